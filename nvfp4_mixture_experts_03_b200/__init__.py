@@ -6,7 +6,9 @@ CPU fallback: importing works without a GPU, but every call that needs the
 library raises if it is missing or was not built.
 
 Low-level names mirror the C ABI (``nvfp4_moe_create``, ``nvfp4_moe_forward``,
-...). ``MoELayer`` wraps one handle together with the tensors it borrows.
+...). ``MoELayer`` wraps one handle together with the tensors it borrows. The 8-bit and
+ragged products beside the layer (``quantize_int8``, ``gemm_int8``, ``grouped_gemm`` and its
+gradients) are in ``products.py`` and are reached from here.
 """
 from __future__ import annotations
 
@@ -32,7 +34,9 @@ EXPORTS = ("nvfp4_moe_create", "nvfp4_moe_workspace_bytes", "nvfp4_moe_forward",
            "nvfp4_moe_get_status", "nvfp4_moe_destroy", "nvfp4_moe_strerror",
            "nvfp4_moe_abi_version", "nvfp4_moe_set_phase_events",
            "nvfp4_moe_forward_decode_static", "nvfp4_moe_forward_decode_stack",
-           "nvfp4_moe_test_set_flags", "nvfp4_moe_test_fail_alloc", "nvfp4_moe_test_last_detail")
+           "nvfp4_moe_test_set_flags", "nvfp4_moe_test_fail_alloc", "nvfp4_moe_test_last_detail",
+           "nvfp4_moe_quantize_int8", "nvfp4_moe_grouped_gemm", "nvfp4_moe_grouped_gemm_dx",
+           "nvfp4_moe_grouped_gemm_dw")
 TEST_DECODE_STALL = 1   # include/nvfp4_moe_test.h
 TEST_NO_SMALL = 2       # every used expert takes the grouped-GEMM tiles
 PHASE_EVENTS = 5
@@ -99,6 +103,10 @@ def lib() -> C.CDLL:
         L.nvfp4_moe_forward_decode_static.restype = C.c_int
         L.nvfp4_moe_forward_decode_static.argtypes = [C.POINTER(Dims), C.POINTER(Weights),
                                                       C.POINTER(IO), C.c_void_p]
+        for name in ("nvfp4_moe_quantize_int8", "nvfp4_moe_grouped_gemm", "nvfp4_moe_grouped_gemm_dx",
+                     "nvfp4_moe_grouped_gemm_dw"):
+            getattr(L, name).restype = C.c_int
+            getattr(L, name).argtypes = [C.c_void_p, C.c_void_p]
         _lib = L
     return _lib
 
@@ -301,3 +309,8 @@ def debug_buffers(T: int, E: int, K: int, device) -> dict:
             "counts": torch.empty(E, **i32), "offsets": torch.empty(E + 1, **i32),
             "perm": torch.empty(T * K, **i32),
             "logits": torch.empty(T, E, dtype=torch.float32, device=device)}
+
+
+from .products import (GemmIO, QuantizeIO, gemm_int8, grouped_gemm, grouped_gemm_dw,  # noqa: E402,F401
+                       grouped_gemm_dx, nvfp4_moe_grouped_gemm, nvfp4_moe_grouped_gemm_dw,
+                       nvfp4_moe_grouped_gemm_dx, nvfp4_moe_quantize_int8, quantize_int8)

@@ -1,0 +1,55 @@
+// Launch parameters shared by the 8-bit and ragged products' host code and kernels.
+#pragma once
+#include "common.cuh"
+#include "nvfp4_moe_products.h"
+
+namespace nvmoe {
+
+// What a product computes (out has contiguous columns):
+//   kFwd  out[p][j] = sum_c x[p][c] w[e][j][c]      rows p of group e, columns j < n, c < k
+//   kDx   out[p][j] = sum_c dy[p][c] w[e][c][j]     rows p of group e, columns j < k, c < n
+//   kDw   out[e][i][j] = sum_p dy[p][i] x[p][j]     rows i < n, columns j < k, p of group e
+enum ProductMode : int { kFwd = 0, kDx = 1, kDw = 2 };
+
+struct Product {
+    int32_t groups, rows, n, k;
+    int32_t out_add;
+    const int32_t *offsets;   // null: one group of all rows
+    const void *x, *dy, *w;
+    int64_t x_ld, dy_ld, w_ld, out_ld;   // row strides in elements
+    const float *x_scale, *w_scale;
+    void *out;
+};
+
+// First and one-past-last row of group e, clamped into [0, rows].
+__device__ inline int2 group_rows(const Product &p, int e) {
+    if (!p.offsets) return make_int2(0, p.rows);
+    const int lo = min(max(p.offsets[e], 0), p.rows);
+    return make_int2(lo, min(max(p.offsets[e + 1], lo), p.rows));
+}
+
+template <typename T>
+__device__ inline float to_f32(T v);
+template <>
+__device__ inline float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ inline float to_f32(__half v) { return __half2float(v); }
+template <>
+__device__ inline float to_f32(float v) { return v; }
+template <>
+__device__ inline float to_f32(int8_t v) { return (float)v; }
+
+template <typename T>
+__device__ inline T from_f32(float v);
+template <>
+__device__ inline __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ inline __half from_f32(float v) { return __float2half_rn(v); }
+template <>
+__device__ inline float from_f32(float v) { return v; }
+
+cudaError_t launch_quantize(const nvfp4_moe_quantize_io &io, cudaStream_t s);
+cudaError_t launch_product(int mode, const Product &p, nvfp4_moe_type type, nvfp4_moe_type out_type,
+                           cudaStream_t s);
+
+}  // namespace nvmoe
