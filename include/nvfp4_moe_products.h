@@ -22,7 +22,8 @@
  * Rows are grouped as nvfp4_moe_forward's dbg_offsets gives them: rows
  * offsets[e] .. offsets[e+1]-1 belong to expert e. The offsets live on the device and
  * are never read back. They must not decrease and must stay within [0, rows]; each is
- * clamped into that range, so wrong ones give wrong rows, but no access out of range.
+ * clamped into that range and to no less than those before it, so wrong ones give wrong
+ * rows, but no access out of range.
  * Rows before offsets[0] and from offsets[groups] on belong to nobody: they are not
  * written (grouped_gemm, dx) and add nothing (dw), whatever they hold.
  *
@@ -128,6 +129,13 @@ typedef struct {
 NVFP4_MOE_API int nvfp4_moe_grouped_gemm(const nvfp4_moe_gemm_io *io, void *stream);
 NVFP4_MOE_API int nvfp4_moe_grouped_gemm_dx(const nvfp4_moe_gemm_io *io, void *stream);
 NVFP4_MOE_API int nvfp4_moe_grouped_gemm_dw(const nvfp4_moe_gemm_io *io, void *stream);
+
+/* Synchronises `stream` and returns the first device-side error that a call of this
+ * header latched on the current device since the last such read (0 if none), clearing
+ * it. The only one there is: NVFP4_MOE_ERR_TIMEOUT, a bounded wait of a product that gave
+ * up, whose output is then not complete. (The products need no handle, so the word
+ * belongs to the device; the layer's own status is nvfp4_moe_get_status.) */
+NVFP4_MOE_API int nvfp4_moe_products_status(void *stream);
 
 #ifdef __cplusplus
 }

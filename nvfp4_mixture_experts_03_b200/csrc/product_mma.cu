@@ -1,0 +1,649 @@
+// Products grouped by expert on the 5th-generation tensor cores (tcgen05 + TMEM): the
+// product itself (16-bit and int8) and both gradients, one kernel.
+//
+// The accumulator D [M][N] holds the output transposed: its M rows (TMEM lanes) are the
+// output's contiguous columns, its N columns are output rows. The ragged side, the rows of
+// a group, is then the MMA's N, which takes any multiple of 16 (an expert with 20 rows
+// costs 32 columns, not a 128-row tile), and a warp stores 32 neighbouring outputs of a
+// row at a time. Operands, c the summed index:
+//   product  A = w[e] (rows j, K-major),   B = x rows (K-major),    c = k
+//   dx       A = w[e]^T (M-major: j runs along w's rows), B = dy rows (K-major), c = n
+//   dw       A = x^T (M-major), B = dy^T (N-major), c = the rows of the group
+// All of them are boxes of 128 bytes x rows in the 128-byte swizzle, by TMA from the
+// tensors as they are; zero fill past n and k, so that neither needs to be a multiple of
+// anything. Rows past a group's end are the next group's: in the product and in dx they
+// give columns of D that nobody reads, in dw they are the sum's tail, and one warp zeroes
+// them in shared memory (both operands: they may hold NaN) before the MMA sees them.
+//
+// A CTA, or a pair of CTAs as one cta_group::2 (then M = 256, each CTA holding 128 rows
+// of A and half of B's columns: half the shared-memory traffic per MMA), walks its tiles
+// in a fixed stride over all groups' tiles, which every CTA lists for itself from the
+// offsets at its start: no host read-back, no workspace, no second launch. The sums'
+// order does not depend on timing.
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "products.cuh"
+
+namespace nvmoe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAccCols = 256;           // two accumulators of up to 256 columns
+constexpr int kTmemCols = 2 * kAccCols;
+constexpr int kLine = 128;              // bytes of a stage's K (or M, N) extent: one swizzle row
+constexpr int kABytes = 128 * kLine;    // A: 128 rows (K-major) or 2 x 64 columns x 64 rows
+constexpr int kMaxStages = 10;
+constexpr size_t kSmemLimit = 227 * 1024;
+constexpr uint64_t kDrainNs = 200000000ull;
+constexpr uint64_t kSettleNs = 1000000ull;   // lets in-flight copies land after an abort
+
+// Latched code and detail of a wait that gave up, per device.
+__device__ int32_t g_status[kStatusWords];
+
+struct MmaParams {
+    Product p;
+    uint32_t idesc;        // instruction descriptor without its N
+    int32_t out_type;
+    int32_t bn;            // most rows of a tile (N); a multiple of 64 per CTA for dw
+    int32_t box;           // rows of one K-major B box
+    int32_t stages;
+};
+
+struct __align__(8) Bars {
+    uint64_t full[kMaxStages];    // leader: one arrival per CTA of the group, and all their bytes
+    uint64_t empty[kMaxStages];   // each CTA: the MMAs' commit
+    uint64_t tail[kMaxStages];    // dw, each CTA: its own bytes of a stage with rows to zero
+    uint64_t acc_full[2];         // each CTA: the MMAs' commit
+    uint64_t acc_empty[2];        // leader: 4 epilogue warps of each CTA
+    uint64_t drain;
+    uint32_t tmem_slot;
+    int abort;
+};
+
+// The groups' rows, and the number of row tiles before each.
+struct Groups {
+    int32_t lo[NVFP4_MOE_MAX_GROUPS];
+    int32_t count[NVFP4_MOE_MAX_GROUPS];
+    int32_t before[NVFP4_MOE_MAX_GROUPS + 1];
+    int32_t warp_sum[kThreads / 32], warp_max[kThreads / 32];
+};
+
+inline size_t stage_bytes(int bn, int cg) { return kABytes + (size_t)bn / cg * kLine; }
+inline size_t smem_bytes(int bn, int cg, int stages) {
+    return 1024 + stages * stage_bytes(bn, cg) + sizeof(Bars) + sizeof(Groups);
+}
+
+template <int CG>
+__device__ inline void tma_3d(void *dst, const CUtensorMap *map, uint64_t *bar, uint32_t bar_leader, int x, int y, int z) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+                smem_u32(dst)),
+            "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+            "l"((uint64_t)map), "r"(bar_leader), "r"(x), "r"(y), "r"(z)
+            : "memory");
+}
+
+template <int CG, bool kI8>
+__device__ inline void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    if (CG == 1 && !kI8)
+        asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                     " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(acc));
+    else if (CG == 2 && !kI8)
+        tc_mma_f16_pair(d, a, b, idesc, acc);
+    else if (CG == 1)
+        asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                     " tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(acc));
+    else
+        asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                     " tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+                     "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+
+// Arrives on `bar` (in every CTA of the group) once the MMAs issued so far are done.
+template <int CG>
+__device__ inline void commit(uint64_t *bar) {
+    if (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                     : "memory");
+    else
+        tc_commit_pair_mc(bar, 0x3);
+}
+
+template <int CG>
+__device__ inline void tmem_alloc(uint32_t *slot) {
+    if (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        tmem_alloc_pair(slot, kTmemCols);
+        tmem_relinquish_pair();
+    }
+}
+template <int CG>
+__device__ inline void tmem_dealloc(uint32_t t) {
+    if (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(kTmemCols));
+    else
+        tmem_dealloc_pair(t, kTmemCols);
+}
+
+// Arrival on a barrier of the leader CTA; writes of this thread (and those it has
+// synchronised with) are visible to who waits there.
+template <int CG>
+__device__ inline void arrive_leader(uint64_t *bar) {
+    if (CG == 1)
+        mbar_arrive(bar);
+    else
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(bar, 0)) : "memory");
+}
+
+// Shared-memory descriptor of an M-major (N-major) operand in the 128-byte swizzle: 64
+// columns to a 128-byte row, 8 rows of c to a 1024-byte group (stride byte offset), the
+// next 64 columns after the 64 rows of this box (leading byte offset).
+__device__ inline uint64_t desc_mn(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(64 * kLine >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// A bounded wait by a whole warp, with one answer for all its lanes.
+template <bool kCluster>
+__device__ inline bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where) {
+    return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, abort, g_status, where));
+}
+
+struct OutTile {
+    int32_t e;       // group
+    int32_t m0;      // first output column
+    int32_t row0;    // first output row: of all rows (product, dx), of the group's matrix (dw)
+    int32_t nrow;    // output rows of the tile (1..bn)
+    int32_t c0, c;   // the summed index: first and count (dw: the group's rows)
+};
+
+template <int MODE, int CG>
+struct Tiles {
+    const MmaParams &q;
+    const Groups &g;
+    int mt, total;   // column tiles; all tiles
+    __device__ Tiles(const MmaParams &q_, const Groups &g_) : q(q_), g(g_) {
+        mt = cdiv(MODE == kFwd ? q.p.n : q.p.k, 128 * CG);
+        total = mt * (MODE == kDw ? q.p.groups * cdiv(q.p.n, q.bn) : g.before[q.p.groups]);
+    }
+    // Tile i, by a whole warp.
+    __device__ OutTile at(int i) const {
+        OutTile t;
+        const int r = i / mt, lane = threadIdx.x & 31;
+        t.m0 = (i - r * mt) * 128 * CG;
+        if (MODE == kDw) {
+            const int nt = cdiv(q.p.n, q.bn);
+            t.e = r / nt;
+            t.row0 = (r - t.e * nt) * q.bn;
+            t.nrow = min(q.bn, q.p.n - t.row0);
+            t.c0 = g.lo[t.e];
+            t.c = g.count[t.e];
+        } else {
+            // the last group with before[e] <= r: first among every 32nd, then among 32
+            const int E = q.p.groups;
+            const int hi = __popc(__ballot_sync(0xffffffffu, 32 * lane < E && g.before[32 * lane] <= r)) - 1;
+            const int c = 32 * hi + lane;
+            t.e = 32 * hi + __popc(__ballot_sync(0xffffffffu, c < E && g.before[min(c, E)] <= r)) - 1;
+            // the group's rows in equal tiles, whole multiples of 16 per CTA
+            const int n = g.before[t.e + 1] - g.before[t.e], cnt = g.count[t.e];
+            const int each = cdiv(cdiv(cnt, n), 16 * CG) * 16 * CG, first = (r - g.before[t.e]) * each;
+            t.row0 = g.lo[t.e] + first;
+            t.nrow = max(0, min(each, cnt - first));
+            t.c0 = 0;
+            t.c = MODE == kFwd ? q.p.k : q.p.n;
+        }
+        return t;
+    }
+};
+
+template <typename O>
+__device__ inline void store_rows(O *o, int64_t ld, const float (&v)[32], int nrow, bool add) {
+    if (add) {
+        float b[32];
+#pragma unroll
+        for (int j = 0; j < 32; j++) b[j] = j < nrow ? to_f32(o[j * ld]) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; j++)
+            if (j < nrow) o[j * ld] = from_f32<O>(v[j] + b[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; j++)
+            if (j < nrow) o[j * ld] = from_f32<O>(v[j]);
+    }
+}
+
+template <int MODE, bool kI8, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_mma_kernel(const __grid_constant__ MmaParams q, const __grid_constant__ CUtensorMap map_a,
+                       const __grid_constant__ CUtensorMap map_b) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t b_bytes = (uint32_t)q.bn / CG * kLine, stage_size = kABytes + b_bytes;
+    Bars *bars = reinterpret_cast<Bars *>(smem + q.stages * stage_size);
+    Groups *groups = reinterpret_cast<Groups *>(bars + 1);
+    volatile int *abort = &bars->abort;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
+    const int cid = (int)blockIdx.x / CG, ncl = (int)gridDim.x / CG;
+    const int S = q.stages;
+    constexpr int kStep = kI8 ? 128 : 64;   // the summed index's extent of a stage
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; s++) {
+            mbar_init(&bars->full[s], CG);
+            mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->tail[s], 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], 4 * CG);
+        }
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 6) tmem_alloc<CG>(&bars->tmem_slot);
+    if (warp == 4 && lane == 0) {
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+    }
+    {   // The groups' rows and row tiles, four groups a thread: offsets clamped into the
+        // rows and to no less than those before them (a running maximum), then summed.
+        constexpr int kPer = NVFP4_MOE_MAX_GROUPS / kThreads;
+        const int E = q.p.groups, e0 = kPer * threadIdx.x;
+        int off[kPer + 1], top = 0;
+#pragma unroll
+        for (int i = 0; i <= kPer; i++) {
+            off[i] = e0 + i > E ? 0 : q.p.offsets ? min(max(q.p.offsets[e0 + i], 0), q.p.rows) : e0 + i ? q.p.rows : 0;
+            top = max(top, off[i]);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) top = max(top, __shfl_up_sync(0xffffffffu, top, d));   // (itself below d)
+        if (lane == 31) groups->warp_max[warp] = top;
+        __syncthreads();
+        int run = __shfl_up_sync(0xffffffffu, top, 1);
+        if (lane == 0) run = 0;
+        for (int w = 0; w < warp; w++) run = max(run, groups->warp_max[w]);
+        int tiles[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            run = max(run, off[i]);
+            const int count = max(off[i + 1] - run, 0);
+            if (e0 + i < E) {
+                groups->lo[e0 + i] = run;
+                groups->count[e0 + i] = count;
+            }
+            tiles[i] = e0 + i < E ? cdiv(count, q.bn) : 0;
+            sum += tiles[i];
+        }
+        int upto = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        if (lane == 31) groups->warp_sum[warp] = upto;
+        __syncthreads();
+        upto -= sum;
+        for (int w = 0; w < warp; w++) upto += groups->warp_sum[w];
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            if (e0 + i <= E) groups->before[e0 + i] = upto;
+            upto += tiles[i];
+        }
+        // with the most groups the total has no thread of its own
+        if (e0 + kPer == E) groups->before[E] = upto;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();   // both CTAs' barriers initialised and TMEM allocated
+    tc_fence_after();
+    const uint32_t tmem_base = bars->tmem_slot;
+    const Tiles<MODE, CG> tiles(q, *groups);
+    int stage = 0;
+    uint32_t phase = 0;
+    auto next = [&]() {
+        if (++stage == S) { stage = 0; phase ^= 1; }
+    };
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ TMA
+        uint32_t issued = 0, issued_phase = 0;   // stages loaded, and the parity of their last use
+        bool ok = true;
+        for (int i = cid; ok && i < tiles.total; i += ncl) {
+            const OutTile t = tiles.at(i);
+            const int half = cdiv(t.nrow, 16 * CG) * 16;   // B columns of this CTA
+            const int brow = t.row0 + rank * half, acol = t.m0 + rank * 128;
+            const int nbox = MODE == kDw ? cdiv(half, 64) : cdiv(half, q.box);
+            const uint32_t bytes = kABytes + nbox * (MODE == kDw ? 64 : q.box) * kLine;
+            for (int c = 0; c < t.c; c += kStep) {
+                if (!warp_wait<CG == 2>(&bars->empty[stage], phase ^ 1, abort, 1)) { ok = false; break; }
+                if (lane == 0) {
+                    uint8_t *a = smem + stage * stage_size, *b = a + kABytes;
+                    const bool tail = MODE == kDw && t.c - c < kStep && ((t.c - c) & 15);
+                    uint64_t *bar = tail ? &bars->tail[stage] : &bars->full[stage];
+                    const uint32_t leader = CG == 1 ? 0 : mapa_shared(bar, tail ? rank : 0);
+                    if (tail)
+                        mbar_arrive_expect_tx(bar, bytes);   // this CTA's own bytes
+                    else if (rank == 0)
+                        mbar_arrive_expect_tx(bar, CG * bytes);
+                    else
+                        arrive_leader<CG>(bar);
+                    issued |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (MODE == kFwd)
+                        tma_3d<CG>(a, &map_a, bar, leader, c, acol, t.e);
+                    else {
+                        for (int h = 0; h < 2; h++)
+                            tma_3d<CG>(a + h * 64 * kLine, &map_a, bar, leader, acol + 64 * h, t.c0 + c, MODE == kDx ? t.e : 0);
+                    }
+                    for (int j = 0; j < nbox; j++) {
+                        if (MODE == kDw)
+                            tma_3d<CG>(b + j * 64 * kLine, &map_b, bar, leader, brow + 64 * j, t.c0 + c, 0);
+                        else
+                            tma_3d<CG>(b + j * q.box * kLine, &map_b, bar, leader, c, brow + j * q.box, 0);
+                    }
+                }
+                __syncwarp();
+                next();
+            }
+        }
+        // The last load of every stage has landed before the CTA ends (after a give-up
+        // nobody else has waited for them).
+        if (rank == 0 && lane == 0)
+            for (int s = 0; s < S; s++)
+                if (issued & (1u << s)) mbar_wait_drain(&bars->full[s], (issued_phase >> s) & 1, kDrainNs);
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------------ MMA (leader)
+        if (rank == 0) {
+            uint32_t acc_phase = 0, it = 0;
+            bool ok = true;
+            for (int i = cid; ok && i < tiles.total; i += ncl) {
+                const OutTile t = tiles.at(i);
+                if (MODE == kDw && t.c == 0) continue;
+                const int buf = it++ & 1;
+                const uint32_t idesc = q.idesc | (uint32_t)(cdiv(t.nrow, 16 * CG) * 2 * CG) << 17;
+                if (!warp_wait<CG == 2>(&bars->acc_empty[buf], ((acc_phase >> buf) & 1) ^ 1, abort, 2)) break;
+                acc_phase ^= 1u << buf;
+                tc_fence_after();
+                const uint32_t d = tmem_base + buf * kAccCols;
+                for (int c = 0; c < t.c; c += kStep) {
+                    if (!warp_wait<CG == 2>(&bars->full[stage], phase, abort, 3)) { ok = false; break; }
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint32_t a = smem_u32(smem + stage * stage_size), b = a + kABytes;
+                        const uint64_t ad = MODE == kFwd ? smem_desc_sw128(a) : desc_mn(a);
+                        const uint64_t bd = MODE == kDw ? desc_mn(b) : smem_desc_sw128(b);
+                        // 32 bytes of K a step, or 16 rows of 128 bytes
+                        constexpr int kA = MODE == kFwd ? 2 : 16 * kLine >> 4, kB = MODE == kDw ? 16 * kLine >> 4 : 2;
+                        const int steps = MODE == kDw ? min(4, cdiv(t.c - c, 16)) : 4;
+#pragma unroll
+                        for (int s = 0; s < 4; s++)
+                            if (s < steps) mma<CG, kI8>(d, ad + s * kA, bd + s * kB, idesc, (c | s) != 0);
+                        commit<CG>(&bars->empty[stage]);
+                    }
+                    __syncwarp();
+                    next();
+                }
+                if (ok && lane == 0) commit<CG>(&bars->acc_full[buf]);
+                __syncwarp();
+            }
+            // every MMA this thread issued completes before TMEM is freed
+            if (lane == 0) {
+                if (CG == 1)
+                    commit<1>(&bars->drain);
+                else
+                    tc_commit_pair(&bars->drain);
+                mbar_wait_drain(&bars->drain, 0, kDrainNs);
+            }
+            __syncwarp();
+        }
+    } else if (warp == 6) {
+        // --------------------------------------- dw: zeroes a group's last rows
+        if (MODE == kDw) {
+            uint32_t tail_phase = 0;
+            bool ok = true;
+            for (int i = cid; ok && i < tiles.total; i += ncl) {
+                const OutTile t = tiles.at(i);
+                const int half = cdiv(t.nrow, 16 * CG) * 16;
+                const int steps = cdiv(t.c, kStep);
+                const int left = t.c - (steps - 1) * kStep;   // rows of the last stage
+                if (t.c && (left & 15)) {
+                    const int last = (stage + steps - 1) % S;
+                    if (!warp_wait<false>(&bars->tail[last], (tail_phase >> last) & 1, abort, 4)) break;
+                    tail_phase ^= 1u << last;
+                    uint8_t *a = smem + last * stage_size, *b = a + kABytes;
+                    const int pad = 16 - (left & 15), nb = cdiv(half, 64);   // rows to zero, in each 64-column box
+                    for (int l = lane; l < pad * (2 + nb) * 8; l += 32) {
+                        const int piece = l & 7, line = l >> 3, box = line / pad, r = left + line - box * pad;
+                        uint8_t *base = box < 2 ? a + box * 64 * kLine : b + (box - 2) * 64 * kLine;
+                        *reinterpret_cast<uint4 *>(base + r * kLine + piece * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_leader<CG>(&bars->full[last]);
+                }
+                stage = (stage + steps) % S;
+            }
+        }
+    } else if (warp < 4) {
+        // -------------------------------------------------------- epilogue
+        uint32_t acc_phase = 0, it = 0;
+        const int cols = MODE == kFwd ? q.p.n : q.p.k;
+        for (int i = cid; i < tiles.total; i += ncl) {
+            const OutTile t = tiles.at(i);
+            const int col = t.m0 + rank * 128 + 32 * warp + lane;
+            const bool mine = col < cols;
+            const bool none = MODE == kDw && t.c == 0;   // an expert without rows: zeros
+            if (none && q.p.out_add) continue;
+            const int64_t at = (MODE == kDw ? (int64_t)t.e * q.p.n + t.row0 : t.row0) * q.p.out_ld + col;
+            const float cs = kI8 && mine ? q.p.w_scale[(int64_t)t.e * q.p.n + col] : 1.0f;
+            const int buf = it & 1;
+            if (!none) {
+                it++;
+                if (!warp_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, 5)) break;
+                acc_phase ^= 1u << buf;
+                tc_fence_after();
+            }
+            const uint32_t tbase = tmem_base + buf * kAccCols + ((uint32_t)(warp * 32) << 16);
+#pragma unroll 1
+            for (int r = 0; r < t.nrow; r += 32) {
+                float v[32];
+                const int n = min(32, t.nrow - r);
+                if (none) {
+#pragma unroll
+                    for (int j = 0; j < 32; j++) v[j] = 0.0f;
+                } else {
+                    uint32_t u[32];
+                    __syncwarp();
+                    tmem_ld32(tbase + r, u);
+                    const float rs = kI8 && lane < n ? q.p.x_scale[t.row0 + r + lane] : 0.0f;
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        v[j] = kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs, j) * cs) : __uint_as_float(u[j]);
+                }
+                if (mine) {
+                    const int64_t o = at + r * q.p.out_ld;
+                    if (q.out_type == NVFP4_MOE_TYPE_F32)
+                        store_rows(static_cast<float *>(q.p.out) + o, q.p.out_ld, v, n, q.p.out_add);
+                    else if (q.out_type == NVFP4_MOE_TYPE_BF16)
+                        store_rows(static_cast<__nv_bfloat16 *>(q.p.out) + o, q.p.out_ld, v, n, false);
+                    else
+                        store_rows(static_cast<__half *>(q.p.out) + o, q.p.out_ld, v, n, false);
+                }
+            }
+            if (!none) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader<CG>(&bars->acc_empty[buf]);
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort) {
+        // after a give-up, copies that were started may still be landing
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < kSettleNs) __nanosleep(1000);
+    }
+    __syncthreads();
+    if (CG == 2) cluster_sync_all();   // no MMA, copy or arrival of the pair touches either CTA past here
+    if (warp == 6) {
+        tc_fence_after();
+        tmem_dealloc<CG>(tmem_base);
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+// [matrices][rows][cols], 128-byte x box_rows boxes in the 128-byte swizzle, zeros outside.
+bool make_map(CUtensorMap *m, const void *base, nvfp4_moe_type type, int64_t cols, int64_t rows, int64_t matrices, int64_t ld,
+              int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const int es = type == NVFP4_MOE_TYPE_INT8 ? 1 : 2;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)matrices};
+    const cuuint64_t strides[2] = {(cuuint64_t)(ld * es), (cuuint64_t)(ld * es * (matrices > 1 ? rows : 1))};
+    const cuuint32_t box[3] = {(cuuint32_t)(kLine / es), (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    const CUtensorMapDataType dt = type == NVFP4_MOE_TYPE_INT8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : type == NVFP4_MOE_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return fn(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+typedef void (*MmaKernel)(const MmaParams, const CUtensorMap, const CUtensorMap);
+
+MmaKernel kernel_of(int mode, bool i8, int cg) {
+    if (i8) return cg == 1 ? product_mma_kernel<kFwd, true, 1> : product_mma_kernel<kFwd, true, 2>;
+    if (mode == kFwd) return cg == 1 ? product_mma_kernel<kFwd, false, 1> : product_mma_kernel<kFwd, false, 2>;
+    if (mode == kDx) return cg == 1 ? product_mma_kernel<kDx, false, 1> : product_mma_kernel<kDx, false, 2>;
+    return cg == 1 ? product_mma_kernel<kDw, false, 1> : product_mma_kernel<kDw, false, 2>;
+}
+
+cudaLaunchConfig_t config(int grid, int cg, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = cg;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cg > 1 ? 1 : 0;
+    return cfg;
+}
+
+// Per device, once: the kernels' shared memory, and how many CTAs and pairs are resident.
+struct Resident {
+    bool done;
+    int ctas, pairs;
+};
+std::mutex g_mu;
+Resident g_resident[64];
+
+cudaError_t resident(Resident *out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(g_mu);
+    Resident &r = g_resident[dev];
+    if (!r.done) {
+        for (int mode = 0; mode < 4; mode++)
+            for (int cg = 1; cg <= 2; cg++) {
+                e = cudaFuncSetAttribute(kernel_of(mode % 3, mode == 3, cg), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemLimit);
+                if (e != cudaSuccess) return e;
+            }
+        e = cudaDeviceGetAttribute(&r.ctas, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute attr;
+        const cudaLaunchConfig_t cfg = config(2, 2, kSmemLimit, 0, &attr);
+        e = cudaOccupancyMaxActiveClusters(&r.pairs, kernel_of(kFwd, false, 2), &cfg);
+        if (e != cudaSuccess) return e;
+        if (r.pairs < 1) return cudaErrorInvalidConfiguration;
+        r.done = true;
+    }
+    *out = r;
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_product(int mode, const Product &p, nvfp4_moe_type type, nvfp4_moe_type out, cudaStream_t s) {
+    if (p.rows == 0) {   // dw: zeros, or nothing added
+        const size_t es = out == NVFP4_MOE_TYPE_F32 ? 4 : 2;
+        if (p.out_add) return cudaSuccess;
+        return cudaMemset2DAsync(p.out, p.out_ld * es, 0, p.k * es, (size_t)p.groups * p.n, s);
+    }
+    Resident r;
+    cudaError_t err = resident(&r);
+    if (err != cudaSuccess) return err;
+    const bool i8 = type == NVFP4_MOE_TYPE_INT8;
+    const int cols = mode == kFwd ? p.n : p.k;
+    MmaParams q{};
+    q.p = p;
+    q.out_type = out;
+    const int avg = mode == kDw ? p.n : cdiv(p.rows, p.groups);
+    const int cg = avg >= 256 && cols > 128 ? 2 : 1;
+    q.bn = cg == 2 ? 256 : avg >= 128 ? 256 : avg > 32 || mode == kDw ? 128 : 64;
+    q.box = 32;
+    q.stages = (int)std::min<size_t>(kMaxStages, (kSmemLimit - smem_bytes(q.bn, cg, 0)) / stage_bytes(q.bn, cg));
+    // D F32 (or S32), A and B F16, BF16 or S8, their majors, M
+    q.idesc = i8 ? (2u << 4) | (1u << 7) | (1u << 10) : (1u << 4) | (type == NVFP4_MOE_TYPE_BF16 ? (1u << 7) | (1u << 10) : 0u);
+    if (mode != kFwd) q.idesc |= 1u << 15;
+    if (mode == kDw) q.idesc |= 1u << 16;
+    q.idesc |= (uint32_t)(128 * cg >> 4) << 24;
+    CUtensorMap a, b;
+    bool ok;
+    if (mode == kFwd)
+        ok = make_map(&a, p.w, type, p.k, p.n, p.groups, p.w_ld, 128) && make_map(&b, p.x, type, p.k, p.rows, 1, p.x_ld, q.box);
+    else if (mode == kDx)
+        ok = make_map(&a, p.w, type, p.k, p.n, p.groups, p.w_ld, 64) && make_map(&b, p.dy, type, p.n, p.rows, 1, p.dy_ld, q.box);
+    else
+        ok = make_map(&a, p.x, type, p.k, p.rows, 1, p.x_ld, 64) && make_map(&b, p.dy, type, p.n, p.rows, 1, p.dy_ld, 64);
+    if (!ok) return cudaErrorInvalidValue;
+    // no more CTAs than there can be tiles
+    const int64_t mt = cdiv(cols, 128 * cg);
+    const int64_t most = mt * (mode == kDw ? (int64_t)p.groups * cdiv(p.n, q.bn)
+                                           : (int64_t)p.rows / q.bn + std::min(p.groups, p.rows));
+    const int units = (int)std::min<int64_t>(cg == 2 ? r.pairs : r.ctas, std::max<int64_t>(most, 1));
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = config(units * cg, cg, smem_bytes(q.bn, cg, q.stages), s, &attr);
+    return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg), q, a, b);
+}
+
+int product_status(cudaStream_t s) {
+    int32_t st[kStatusWords];
+    if (cudaStreamSynchronize(s) != cudaSuccess || cudaMemcpyFromSymbol(st, g_status, sizeof(st)) != cudaSuccess)
+        return NVFP4_MOE_ERR_CUDA;
+    if (st[kStatusCode] != 0) {
+        memset(st + 1, 0, sizeof(st) - sizeof(st[0]));
+        const int32_t code = st[kStatusCode];
+        st[kStatusCode] = 0;
+        if (cudaMemcpyToSymbol(g_status, st, sizeof(st)) != cudaSuccess) return NVFP4_MOE_ERR_CUDA;
+        return code;
+    }
+    return NVFP4_MOE_OK;
+}
+
+}  // namespace nvmoe

@@ -21,13 +21,6 @@ struct Product {
     void *out;
 };
 
-// First and one-past-last row of group e, clamped into [0, rows].
-__device__ inline int2 group_rows(const Product &p, int e) {
-    if (!p.offsets) return make_int2(0, p.rows);
-    const int lo = min(max(p.offsets[e], 0), p.rows);
-    return make_int2(lo, min(max(p.offsets[e + 1], lo), p.rows));
-}
-
 template <typename T>
 __device__ inline float to_f32(T v);
 template <>
@@ -51,5 +44,6 @@ __device__ inline float from_f32(float v) { return v; }
 cudaError_t launch_quantize(const nvfp4_moe_quantize_io &io, cudaStream_t s);
 cudaError_t launch_product(int mode, const Product &p, nvfp4_moe_type type, nvfp4_moe_type out_type,
                            cudaStream_t s);
+int product_status(cudaStream_t s);   // the first wait that gave up on the current device, cleared
 
 }  // namespace nvmoe

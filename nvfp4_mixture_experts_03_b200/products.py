@@ -57,7 +57,17 @@ def nvfp4_moe_grouped_gemm_dw(io: GemmIO, stream: int) -> int:
     return lib().nvfp4_moe_grouped_gemm_dw(C.byref(io), C.c_void_p(stream))
 
 
+def nvfp4_moe_products_status(stream: int) -> int:
+    return lib().nvfp4_moe_products_status(C.c_void_p(stream))
+
+
 # ---------------------------------------------------------------- torch glue
+
+def products_status(stream=None) -> int:
+    """Synchronises and returns the first device-side error of the products on the current
+    device since the last read (0 if none), clearing it."""
+    return nvfp4_moe_products_status((stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
+
 
 def _need(ok: bool, what: str) -> None:
     if not ok:

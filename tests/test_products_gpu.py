@@ -32,6 +32,7 @@ NAN = float("nan")
 def no_tf32():
     assert not torch.backends.cuda.matmul.allow_tf32
     yield
+    assert nv.products_status() == 0      # no bounded wait gave up in any of these tests
 
 
 def gen(seed):
