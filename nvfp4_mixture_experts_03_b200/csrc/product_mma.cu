@@ -589,7 +589,7 @@ cudaError_t resident(Resident *out) {
 
 }  // namespace
 
-cudaError_t launch_product(int mode, const Product &p, nvfp4_moe_type type, nvfp4_moe_type out, cudaStream_t s) {
+cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, nvfp4_moe_type out, cudaStream_t s) {
     if (p.rows == 0) {   // dw: zeros, or nothing added
         const size_t es = out == NVFP4_MOE_TYPE_F32 ? 4 : 2;
         if (p.out_add) return cudaSuccess;

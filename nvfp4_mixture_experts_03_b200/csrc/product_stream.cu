@@ -1,0 +1,186 @@
+// Products of a few rows (single tokens being decoded): the matrices are streamed once
+// through mma.sync, straight from global memory to registers.
+//
+// One CTA computes 16 output columns (16 rows of w[e]) for up to 8 * NT rows of one group,
+// its eight warps splitting k. D = w (16 x K) x^T (K x 8): lane (g, q) of a warp loads 16
+// consecutive bytes of matrix rows g and g + 8 and of x row g; a lane's four words are its
+// operands of two MMAs. Which k a word stands for is the same on both sides, so the
+// products are those of the plain order. The warps' sums are added in warp order: the same
+// bits on every run.
+//
+// Bound by latency, then by memory: nothing is staged or laid out, no tensor map, no
+// barrier but the one before the join, and a warp's loads of a whole k range are in
+// flight before its first MMA waits.
+#include "products.cuh"
+
+namespace nvmoe {
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kCols = 16;
+constexpr int kDeep = 4;   // 16-byte pieces of each row that a lane has in flight
+
+__device__ inline uint4 ld_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Keeps the first n bytes of 16 (what a row holds past its length may be NaN).
+__device__ inline uint4 keep(uint4 v, int n) {
+    uint32_t *w = &v.x;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int b = n - 4 * i;
+        w[i] = b >= 4 ? w[i] : b <= 0 ? 0u : w[i] & ((1u << (8 * b)) - 1);
+    }
+    return v;
+}
+
+__device__ inline void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                             __half) {
+    mma_16816(d, a0, a1, a2, a3, b0, b1);
+}
+__device__ inline void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                             __nv_bfloat16) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ inline void mma16(int32_t (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                             int8_t) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <typename O>
+__device__ inline void put(O *o, float v, bool add) {
+    *o = from_f32<O>(add ? v + to_f32(*o) : v);
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kThreads) product_stream_kernel(const __grid_constant__ Product p, const int out_type) {
+    constexpr bool kI8 = std::is_same<T, int8_t>::value;
+    using Acc = typename std::conditional<kI8, int32_t, float>::type;
+    __shared__ Acc part[kWarps][8 * NT][kCols + 1];
+    const int col0 = blockIdx.x * kCols;
+    // Rows row0 .. row0+nrow-1 of group e: with offsets, block y stands for row y and works
+    // if that row opens a batch of 8 * NT rows of its group.
+    int e = 0, row0 = blockIdx.y * 8 * NT, end = p.rows;
+    if (p.offsets) {
+        row0 = blockIdx.y;
+        int below = 0;
+        for (int i = threadIdx.x; i < p.groups; i += kThreads) below += p.offsets[i] <= row0;
+        below = __reduce_add_sync(0xffffffffu, below);
+        __shared__ int count[kWarps];
+        if ((threadIdx.x & 31) == 0) count[threadIdx.x >> 5] = below;
+        __syncthreads();
+        below = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) below += count[w];
+        if (below == 0) return;
+        e = below - 1;
+        const int lo = max(p.offsets[e], 0);
+        end = min(p.offsets[e + 1], p.rows);
+        if (row0 < lo || row0 >= end || (row0 - lo) % (8 * NT)) return;
+    }
+    const int nrow = min(8 * NT, end - row0);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int64_t kb = (int64_t)p.k * sizeof(T);   // bytes of a row
+    const int64_t w_ld = p.w_ld * sizeof(T), x_ld = p.x_ld * sizeof(T);
+    // Rows past the matrix or the batch repeat its last one; their results are dropped.
+    const char *w0 = static_cast<const char *>(p.w) + ((int64_t)e * p.n + min(col0 + g, p.n - 1)) * w_ld;
+    const char *w1 = static_cast<const char *>(p.w) + ((int64_t)e * p.n + min(col0 + g + 8, p.n - 1)) * w_ld;
+    const char *x[NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) x[t] = static_cast<const char *>(p.x) + (int64_t)(row0 + min(8 * t + g, nrow - 1)) * x_ld;
+
+    Acc acc[NT][4] = {};
+    // 64 bytes of every row a piece, 64 * kDeep bytes a step; the warps take steps in turn.
+    for (int64_t k0 = (int64_t)warp * (64 * kDeep); k0 < kb; k0 += kWarps * 64 * kDeep) {
+        uint4 a0[kDeep], a1[kDeep], b[NT][kDeep];
+#pragma unroll
+        for (int d = 0; d < kDeep; d++) {
+            const int64_t at = k0 + 64 * d + 16 * q;
+            if (at < kb) {
+                a0[d] = ld_stream(w0 + at);
+                a1[d] = ld_stream(w1 + at);
+#pragma unroll
+                for (int t = 0; t < NT; t++) b[t][d] = *reinterpret_cast<const uint4 *>(x[t] + at);
+            } else {
+                a0[d] = a1[d] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < NT; t++) b[t][d] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        if (k0 + 64 * kDeep > kb) {
+#pragma unroll
+            for (int d = 0; d < kDeep; d++) {
+                const int left = (int)max((int64_t)0, min((int64_t)16, kb - (k0 + 64 * d + 16 * q)));
+                a0[d] = keep(a0[d], left);
+                a1[d] = keep(a1[d], left);
+#pragma unroll
+                for (int t = 0; t < NT; t++) b[t][d] = keep(b[t][d], left);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < kDeep; d++)
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                mma16(acc[t], a0[d].x, a1[d].x, a0[d].y, a1[d].y, b[t][d].x, b[t][d].y, T());
+                mma16(acc[t], a0[d].z, a1[d].z, a0[d].w, a1[d].w, b[t][d].z, b[t][d].w, T());
+            }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) part[warp][8 * t + 2 * q + (i & 1)][g + 8 * (i >> 1)] = acc[t][i];
+    __syncthreads();
+#pragma unroll
+    for (int i = threadIdx.x; i < 8 * NT * kCols; i += kThreads) {
+        const int c = i % kCols, r = i / kCols, col = col0 + c;
+        if (r >= nrow || col >= p.n) continue;
+        Acc sum = part[0][r][c];
+#pragma unroll
+        for (int w = 1; w < kWarps; w++) sum += part[w][r][c];
+        float v = (float)sum;
+        if (kI8) v *= p.x_scale[row0 + r] * p.w_scale[(int64_t)e * p.n + col];
+        const int64_t at = (row0 + r) * p.out_ld + col;
+        if (out_type == NVFP4_MOE_TYPE_F32)
+            put(static_cast<float *>(p.out) + at, v, p.out_add);
+        else if (out_type == NVFP4_MOE_TYPE_BF16)
+            put(static_cast<__nv_bfloat16 *>(p.out) + at, v, false);
+        else
+            put(static_cast<__half *>(p.out) + at, v, false);
+    }
+}
+
+template <typename T>
+cudaError_t launch(const Product &p, nvfp4_moe_type out, cudaStream_t s) {
+    // Batches of 8 rows where the rows are spread over groups (most have a row or two) or
+    // are no more than that; a dense call's rows in one batch up to 32.
+    const int nt = p.groups > 1 || p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
+    const dim3 grid(cdiv(p.n, kCols), p.offsets ? p.rows : cdiv(p.rows, 8 * nt));
+    if (nt == 1)
+        product_stream_kernel<T, 1><<<grid, kThreads, 0, s>>>(p, out);
+    else if (nt == 2)
+        product_stream_kernel<T, 2><<<grid, kThreads, 0, s>>>(p, out);
+    else
+        product_stream_kernel<T, 4><<<grid, kThreads, 0, s>>>(p, out);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool product_streams(int mode, const Product &p) { return mode == kFwd && p.rows <= 32; }
+
+cudaError_t launch_product_stream(const Product &p, nvfp4_moe_type type, nvfp4_moe_type out, cudaStream_t s) {
+    return type == NVFP4_MOE_TYPE_INT8   ? launch<int8_t>(p, out, s)
+           : type == NVFP4_MOE_TYPE_BF16 ? launch<__nv_bfloat16>(p, out, s)
+                                         : launch<__half>(p, out, s);
+}
+
+}  // namespace nvmoe

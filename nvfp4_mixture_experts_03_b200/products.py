@@ -69,71 +69,79 @@ def products_status(stream=None) -> int:
     return nvfp4_moe_products_status((stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+# These run before every launch, so what a good call needs is kept short: messages are put
+# together only where a check fails.
+
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stream().cuda_stream, without its object
+_UNIT = {torch.bfloat16: 8, torch.float16: 8, torch.float32: 4, torch.int8: 16}   # values in 16 bytes
 
 
-def _vector(t, n: int, dtype, name: str, device):
-    """The address of a contiguous vector (or matrix) of n values."""
-    _need(t.dtype == dtype and t.numel() == n and t.is_contiguous() and t.device == device,
-          f"{name}: expected {n} contiguous {dtype} values on {device}")
+def _device_of(t, what: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{what}: expected CUDA tensors")
+    return index
+
+
+def _vector(t, n: int, dtype, name: str, index: int) -> int:
+    """The address of n contiguous values."""
+    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} values on cuda:{index}")
     return t.data_ptr()
 
 
-def _rows(t, cols: int, name: str, device):
-    """(address, row stride) of [rows][cols] with contiguous rows."""
-    _need(t.dim() == 2 and t.shape[1] == cols and t.device == device and (cols == 1 or t.stride(1) == 1),
-          f"{name}: expected rows of {cols} contiguous values on {device}")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), _pad(cols, t.dtype)))
+def _row_stride(t, rows: int, cols: int, name: str, index: int) -> int:
+    """The row stride of [rows][cols] with contiguous rows."""
+    if t.dim() != 2 or t.get_device() != index:
+        raise ValueError(f"{name}: expected a matrix on cuda:{index}")
+    ld, step = t.stride()
+    if step != 1 and cols != 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    return ld if rows > 1 else _pad(cols, t.dtype)   # one row: no stride to take
 
 
-def _matrices(t, name: str, device):
-    """(address, row stride) of [groups][n][k] or [n][k] whose matrices follow one another."""
-    _need(t.dim() in (2, 3) and t.device == device and (t.shape[-1] == 1 or t.stride(-1) == 1),
-          f"{name}: expected [groups][n][k] or [n][k] with contiguous rows on {device}")
-    n, k = t.shape[-2:]
-    if t.dim() == 3 and t.shape[0] > 1 and n == 1:
-        ld = t.stride(0)
+def _matrix_stride(t, groups: int, n: int, k: int, name: str, index: int) -> int:
+    """The row stride of [groups][n][k] or [n][k] whose matrices follow one another."""
+    if t.get_device() != index:
+        raise ValueError(f"{name}: expected a tensor on cuda:{index}")
+    stride = t.stride()
+    if stride[-1] != 1 and k != 1:
+        raise ValueError(f"{name}: expected contiguous rows")
+    if n > 1:
+        ld = stride[-2]
     else:
-        ld = t.stride(-2) if n > 1 else max(t.stride(-2), _pad(k, t.dtype))
-        _need(t.dim() == 2 or t.shape[0] <= 1 or t.stride(0) == n * ld,
-              f"{name}: matrices have to follow one another, n rows apart")
-    return t.data_ptr(), ld
+        ld = stride[0] if groups > 1 else _pad(k, t.dtype)
+    if groups > 1 and stride[0] != n * ld:
+        raise ValueError(f"{name}: matrices have to follow one another, n rows apart")
+    return ld
 
 
 def _pad(cols: int, dtype) -> int:
-    unit = 16 // dtype.itemsize
+    unit = _UNIT[dtype]
     return -(-cols // unit) * unit
 
 
-def _new(shape, dtype, device):
-    """An empty tensor whose rows start every whole number of 16 bytes."""
+def _new(shape, dtype, index: int, stream):
+    """An empty tensor whose rows start every whole number of 16 bytes, allocated on `stream`."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _new(shape, dtype, index, None)
     cols = shape[-1]
     ld = _pad(cols, dtype)
-    t = torch.empty(*shape[:-1], ld, dtype=dtype, device=device)
+    t = torch.empty((*shape[:-1], ld), dtype=dtype, device=index)
     return t if ld == cols else t[..., :cols]
 
 
-def _enqueue(what: str, fill, out, shape, dtype, device, stream):
-    """Allocates `out` unless given, and makes the call on the right device and stream.
-    fill(out) -> (function, io)."""
-    if device.type != "cuda":
-        raise ValueError(f"{what}: expected CUDA tensors")
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _enqueue(what, fill, out, shape, dtype, device, stream)
-    if out is None:
-        if stream is None:
-            out = _new(shape, dtype, device)
-        else:
-            with torch.cuda.stream(stream):
-                out = _new(shape, dtype, device)
-    fn, io = fill(out)
-    rc = fn(io, torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream)
+def _enqueue(fn, io, index: int, stream, what: str) -> None:
+    s = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
+        rc = fn(C.byref(io), s)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(C.byref(io), s)
     if rc != OK:
         raise NVFP4MoEError(rc, what)
-    return out
 
 
 def quantize_int8(x, *, swiglu: bool = False, q=None, scale=None, stream=None):
@@ -141,49 +149,58 @@ def quantize_int8(x, *, swiglu: bool = False, q=None, scale=None, stream=None):
     nearest whole number (ties to even). x: [rows][cols] bf16, f16 or f32; with `swiglu`
     [rows][2*cols] holding gate | up, and v = SiLU(gate) * up.
     Returns (q int8 [rows][cols], scale f32 [rows])."""
-    _need(x.dim() == 2 and x.dtype in _TYPES and x.dtype != torch.int8, "x: expected [rows][cols] bf16, f16 or f32")
+    t = _TYPES.get(x.dtype, TYPE_INT8)
+    if x.dim() != 2 or t == TYPE_INT8:
+        raise ValueError("x: expected [rows][cols] bf16, f16 or f32")
     rows, width = x.shape
-    _need(width > 0 and not (swiglu and width % 2), "x: expected at least one value a row (gate | up: an even number)")
+    if width == 0 or (swiglu and width % 2):
+        raise ValueError("x: expected at least one value a row (gate | up: an even number)")
     cols = width // 2 if swiglu else width
-    device = x.device
-    x_ptr, x_ld = _rows(x, width, "x", device)
-    if q is not None:
-        _need(q.dtype == torch.int8 and q.dim() == 2 and q.shape[0] == rows, f"q: expected int8 [{rows}][{cols}]")
-        _rows(q, cols, "q", device)
-    if scale is not None:
-        _vector(scale, rows, torch.float32, "scale", device)
-
-    def fill(q):
-        nonlocal scale
-        if scale is None:
-            if stream is None:
-                scale = torch.empty(rows, dtype=torch.float32, device=device)
-            else:
-                with torch.cuda.stream(stream):
-                    scale = torch.empty(rows, dtype=torch.float32, device=device)
-        return nvfp4_moe_quantize_int8, QuantizeIO(rows, cols, _TYPES[x.dtype], int(swiglu), x_ptr, x_ld, q.data_ptr(),
-                                                   q.stride(0) if rows > 1 else max(q.stride(0), cols), scale.data_ptr())
-
-    q = _enqueue("nvfp4_moe_quantize_int8", fill, q, (rows, cols), torch.int8, device, stream)
+    index = _device_of(x, "quantize_int8")
+    x_ld = _row_stride(x, rows, width, "x", index)
+    if q is None:
+        q = _new((rows, cols), torch.int8, index, stream)
+    elif q.dtype != torch.int8 or tuple(q.shape) != (rows, cols):
+        raise ValueError(f"q: expected int8 [{rows}][{cols}]")
+    q_ld = _row_stride(q, rows, cols, "q", index)
+    if scale is None:
+        if stream is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=index)
+        else:
+            with torch.cuda.stream(stream):
+                scale = torch.empty(rows, dtype=torch.float32, device=index)
+        s_ptr = scale.data_ptr()
+    else:
+        s_ptr = _vector(scale, rows, torch.float32, "scale", index)
+    io = QuantizeIO(rows, cols, t, 1 if swiglu else 0, x.data_ptr(), x_ld, q.data_ptr(), q_ld, s_ptr)
+    _enqueue(lib().nvfp4_moe_quantize_int8, io, index, stream, "nvfp4_moe_quantize_int8")
     return q, scale
 
 
-def _check_out(out, shape, out_dtype, device):
-    if out is None:
-        _need(out_dtype in _TYPES and out_dtype != torch.int8, "out_dtype: expected bf16, f16 or f32")
-        return out_dtype
-    _need(tuple(out.shape) == tuple(shape) and out.dtype in _TYPES and out.dtype != torch.int8
-          and (out_dtype is None or out.dtype == out_dtype), f"out: expected {list(shape)}, bf16, f16 or f32")
-    _need(out.device == device, f"out: expected a tensor on {device}")
-    return out.dtype
+def _out_type(out, shape, out_dtype) -> int:
+    """The output's type, checked against what the caller asked for."""
+    t = _TYPES.get(out_dtype if out is None else out.dtype, TYPE_INT8)
+    if t == TYPE_INT8:
+        raise ValueError("out, out_dtype: expected bf16, f16 or f32")
+    if out is not None and (tuple(out.shape) != shape or (out_dtype is not None and out.dtype != out_dtype)):
+        raise ValueError(f"out: expected {list(shape)}" + (f" of {out_dtype}" if out_dtype is not None else ""))
+    return t
 
 
-def _groups(offsets, w_shape, device):
-    groups = w_shape[0] if len(w_shape) == 3 else 1
+def _offsets(offsets, groups: int, index: int):
     if offsets is None:
-        _need(groups == 1, "offsets: needed for more than one group")
-        return groups, None
-    return groups, _vector(offsets, groups + 1, torch.int32, "offsets", device)
+        if groups != 1:
+            raise ValueError("offsets: needed for more than one group")
+        return None
+    return _vector(offsets, groups + 1, torch.int32, "offsets", index)
+
+
+def _operands(x, w, names: str):
+    """(groups, rows, n, k) of rows x and matrices w."""
+    if x.dim() != 2 or w.dim() not in (2, 3) or x.dtype != w.dtype:
+        raise ValueError(f"{names}: expected a matrix of rows, [groups][n][k] or [n][k], and one type")
+    n, k = w.shape[-2:]
+    return (w.shape[0] if w.dim() == 3 else 1), x.shape[0], n, k
 
 
 def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, out_dtype=None,
@@ -192,37 +209,42 @@ def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, ou
     (or [n][k]), both bf16, f16, or int8 with x_scale [rows] and w_scale [groups][n] f32.
     out: [rows][n], by default of x's type (f32 for int8); rows of no group are not written.
     accumulate: out += (f32)."""
-    _need(w.dim() in (2, 3) and x.dim() == 2, "expected x [rows][k] and w [groups][n][k] or [n][k]")
-    _need(x.dtype == w.dtype and x.dtype in _TYPES and x.dtype != torch.float32,
-          "x and w: expected the same type, bf16, f16 or int8")
-    _need(not accumulate or out is not None, "accumulate: needs out")
-    device, rows, (n, k) = x.device, x.shape[0], w.shape[-2:]
-    groups, off = _groups(offsets, w.shape, device)
-    x_ptr, x_ld = _rows(x, k, "x", device)
-    w_ptr, w_ld = _matrices(w, "w", device)
+    groups, rows, n, k = _operands(x, w, "x, w")
+    t = _TYPES.get(x.dtype, TYPE_F32)
+    if t == TYPE_F32 or x.shape[1] != k:
+        raise ValueError("x, w: expected [rows][k] and [groups][n][k], bf16, f16 or int8")
+    index = _device_of(x, "grouped_gemm")
+    off = _offsets(offsets, groups, index)
+    x_ld = _row_stride(x, rows, k, "x", index)
+    w_ld = _matrix_stride(w, groups, n, k, "w", index)
     xs = ws = None
-    if x.dtype == torch.int8:
-        _need(x_scale is not None and w_scale is not None, "int8: needs x_scale and w_scale")
-        xs = _vector(x_scale, rows, torch.float32, "x_scale", device)
-        ws = _vector(w_scale, groups * n, torch.float32, "w_scale", device)
+    if t == TYPE_INT8:
+        if x_scale is None or w_scale is None:
+            raise ValueError("int8: needs x_scale and w_scale")
+        xs = _vector(x_scale, rows, torch.float32, "x_scale", index)
+        ws = _vector(w_scale, groups * n, torch.float32, "w_scale", index)
+    elif x_scale is not None or w_scale is not None:
+        raise ValueError("x_scale, w_scale: for int8 only")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate: needs out")
+        if out_dtype is None:
+            out_dtype = torch.float32 if t == TYPE_INT8 else x.dtype
+        o = _out_type(None, None, out_dtype)
+        out = _new((rows, n), out_dtype, index, stream)
     else:
-        _need(x_scale is None and w_scale is None, "x_scale, w_scale: for int8 only")
-    if out is None and out_dtype is None:
-        out_dtype = torch.float32 if x.dtype == torch.int8 else x.dtype
-    dtype = _check_out(out, (rows, n), out_dtype, device)
-
-    def fill(out):
-        o_ptr, o_ld = _rows(out, n, "out", device)
-        return nvfp4_moe_grouped_gemm, GemmIO(groups, rows, n, k, _TYPES[x.dtype], _TYPES[dtype], int(accumulate), off,
-                                              x_ptr, x_ld, xs, None, 0, w_ptr, w_ld, ws, o_ptr, o_ld)
-
-    return _enqueue("nvfp4_moe_grouped_gemm", fill, out, (rows, n), dtype, device, stream)
+        o = _out_type(out, (rows, n), out_dtype)
+    io = GemmIO(groups, rows, n, k, t, o, 1 if accumulate else 0, off, x.data_ptr(), x_ld, xs, None, 0, w.data_ptr(), w_ld,
+                ws, out.data_ptr(), _row_stride(out, rows, n, "out", index))
+    _enqueue(lib().nvfp4_moe_grouped_gemm, io, index, stream, "nvfp4_moe_grouped_gemm")
+    return out
 
 
 def gemm_int8(x, w, x_scale, w_scale, *, out=None, out_dtype=None, accumulate: bool = False, stream=None):
     """out[t][j] = x_scale[t] * w_scale[j] * sum_k x[t][k] w[j][k], the sum exact. x: [rows][k]
     int8, w: [n][k] int8, scales f32. out: [rows][n], f32 by default. accumulate: out += (f32)."""
-    _need(x.dtype == torch.int8 and w.dtype == torch.int8 and w.dim() == 2, "expected int8 x [rows][k] and w [n][k]")
+    if x.dtype != torch.int8 or w.dim() != 2:
+        raise ValueError("x, w: expected int8 [rows][k] and [n][k]")
     return grouped_gemm(x, w, None, x_scale=x_scale, w_scale=w_scale, out=out, out_dtype=out_dtype,
                         accumulate=accumulate, stream=stream)
 
@@ -230,41 +252,51 @@ def gemm_int8(x, w, x_scale, w_scale, *, out=None, out_dtype=None, accumulate: b
 def grouped_gemm_dx(dy, w, offsets=None, *, out=None, out_dtype=None, accumulate: bool = False, stream=None):
     """The gradient of grouped_gemm for x: dx[p] = dy[p] W_e. dy: [rows][n], w: [groups][n][k],
     both bf16 or f16. out: [rows][k], by default of dy's type; rows of no group are not written."""
-    _need(w.dim() in (2, 3) and dy.dim() == 2, "expected dy [rows][n] and w [groups][n][k] or [n][k]")
-    _need(dy.dtype == w.dtype and dy.dtype in (torch.bfloat16, torch.float16), "dy and w: expected the same type, bf16 or f16")
-    _need(not accumulate or out is not None, "accumulate: needs out")
-    device, rows, (n, k) = dy.device, dy.shape[0], w.shape[-2:]
-    groups, off = _groups(offsets, w.shape, device)
-    dy_ptr, dy_ld = _rows(dy, n, "dy", device)
-    w_ptr, w_ld = _matrices(w, "w", device)
-    dtype = _check_out(out, (rows, k), out_dtype or (None if out is not None else dy.dtype), device)
-
-    def fill(out):
-        o_ptr, o_ld = _rows(out, k, "out", device)
-        return nvfp4_moe_grouped_gemm_dx, GemmIO(groups, rows, n, k, _TYPES[dy.dtype], _TYPES[dtype], int(accumulate), off,
-                                                 None, 0, None, dy_ptr, dy_ld, w_ptr, w_ld, None, o_ptr, o_ld)
-
-    return _enqueue("nvfp4_moe_grouped_gemm_dx", fill, out, (rows, k), dtype, device, stream)
+    groups, rows, n, k = _operands(dy, w, "dy, w")
+    t = _TYPES.get(dy.dtype, TYPE_F32)
+    if t not in (TYPE_BF16, TYPE_F16) or dy.shape[1] != n:
+        raise ValueError("dy, w: expected [rows][n] and [groups][n][k], bf16 or f16")
+    index = _device_of(dy, "grouped_gemm_dx")
+    off = _offsets(offsets, groups, index)
+    dy_ld = _row_stride(dy, rows, n, "dy", index)
+    w_ld = _matrix_stride(w, groups, n, k, "w", index)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate: needs out")
+        out_dtype = dy.dtype if out_dtype is None else out_dtype
+        o = _out_type(None, None, out_dtype)
+        out = _new((rows, k), out_dtype, index, stream)
+    else:
+        o = _out_type(out, (rows, k), out_dtype)
+    io = GemmIO(groups, rows, n, k, t, o, 1 if accumulate else 0, off, None, 0, None, dy.data_ptr(), dy_ld, w.data_ptr(), w_ld,
+                None, out.data_ptr(), _row_stride(out, rows, k, "out", index))
+    _enqueue(lib().nvfp4_moe_grouped_gemm_dx, io, index, stream, "nvfp4_moe_grouped_gemm_dx")
+    return out
 
 
 def grouped_gemm_dw(dy, x, offsets=None, *, out=None, out_dtype=None, accumulate: bool = False, stream=None):
     """The gradient of grouped_gemm for w: dW_e = sum over the rows p of e of dy[p]^T x[p].
     dy: [rows][n], x: [rows][k], both bf16 or f16. out: [groups][n][k] ([n][k] without
     offsets), f32 by default; zeros for a group without rows. accumulate: out += (f32)."""
-    _need(dy.dim() == 2 and x.dim() == 2 and dy.shape[0] == x.shape[0], "expected dy [rows][n] and x [rows][k]")
-    _need(dy.dtype == x.dtype and dy.dtype in (torch.bfloat16, torch.float16), "dy and x: expected the same type, bf16 or f16")
-    _need(not accumulate or out is not None, "accumulate: needs out")
-    _need(offsets is None or (offsets.dim() == 1 and offsets.numel() >= 2), "offsets: expected groups + 1 entries")
-    device, rows, n, k = x.device, x.shape[0], dy.shape[1], x.shape[1]
-    shape = (n, k) if offsets is None else (offsets.numel() - 1, n, k)
-    groups, off = _groups(offsets, shape, device)
-    dy_ptr, dy_ld = _rows(dy, n, "dy", device)
-    x_ptr, x_ld = _rows(x, k, "x", device)
-    dtype = _check_out(out, shape, out_dtype or (None if out is not None else torch.float32), device)
-
-    def fill(out):
-        o_ptr, o_ld = _matrices(out, "out", device)
-        return nvfp4_moe_grouped_gemm_dw, GemmIO(groups, rows, n, k, _TYPES[x.dtype], _TYPES[dtype], int(accumulate), off,
-                                                 x_ptr, x_ld, None, dy_ptr, dy_ld, None, 0, None, o_ptr, o_ld)
-
-    return _enqueue("nvfp4_moe_grouped_gemm_dw", fill, out, shape, dtype, device, stream)
+    t = _TYPES.get(dy.dtype, TYPE_F32)
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or dy.dtype != x.dtype or t not in (TYPE_BF16, TYPE_F16):
+        raise ValueError("dy, x: expected [rows][n] and [rows][k], both bf16 or f16")
+    index = _device_of(x, "grouped_gemm_dw")
+    (rows, k), n = x.shape, dy.shape[1]
+    groups = 1 if offsets is None else offsets.numel() - 1
+    off = _offsets(offsets, groups, index)
+    dy_ld = _row_stride(dy, rows, n, "dy", index)
+    x_ld = _row_stride(x, rows, k, "x", index)
+    shape = (n, k) if offsets is None else (groups, n, k)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate: needs out")
+        out_dtype = torch.float32 if out_dtype is None else out_dtype
+        o = _out_type(None, None, out_dtype)
+        out = _new(shape, out_dtype, index, stream)
+    else:
+        o = _out_type(out, shape, out_dtype)
+    io = GemmIO(groups, rows, n, k, t, o, 1 if accumulate else 0, off, x.data_ptr(), x_ld, None, dy.data_ptr(), dy_ld, None, 0,
+                None, out.data_ptr(), _matrix_stride(out, groups, n, k, "out", index))
+    _enqueue(lib().nvfp4_moe_grouped_gemm_dw, io, index, stream, "nvfp4_moe_grouped_gemm_dw")
+    return out
