@@ -29,7 +29,10 @@
 namespace nvmoe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kEpiWarps = 8;            // two for each quarter of the TMEM lanes
+constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kTailWarp = kEpiWarps + 2;
+constexpr int kThreads = 32 * (kEpiWarps + 4);
+constexpr int kScanThreads = 256;       // of the CTA's, list the groups
 constexpr int kAccCols = 256;           // two accumulators of up to 256 columns
 constexpr int kTmemCols = 2 * kAccCols;
 constexpr int kLine = 128;              // bytes of a stage's K (or M, N) extent: one swizzle row
@@ -52,11 +55,12 @@ struct MmaParams {
 };
 
 struct __align__(8) Bars {
-    uint64_t full[kMaxStages];    // leader: one arrival per CTA of the group, and all their bytes
+    uint64_t full[kMaxStages];    // leader: its one arrival, and the bytes of every CTA of the group
     uint64_t empty[kMaxStages];   // each CTA: the MMAs' commit
     uint64_t tail[kMaxStages];    // dw, each CTA: its own bytes of a stage with rows to zero
+    uint64_t peer[kMaxStages];    // dw, leader: the other CTA has zeroed its rows of a stage
     uint64_t acc_full[2];         // each CTA: the MMAs' commit
-    uint64_t acc_empty[2];        // leader: 4 epilogue warps of each CTA
+    uint64_t acc_empty[2];        // leader: the epilogue warps of each CTA
     uint64_t drain;
     uint32_t tmem_slot;
     int abort;
@@ -155,6 +159,19 @@ __device__ inline uint64_t desc_mn(uint32_t saddr) {
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// Has the phase with this parity completed? Does not wait.
+template <bool kCluster>
+__device__ inline bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    if (kCluster)
+        asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    else
+        asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                     : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // A bounded wait by a whole warp, with one answer for all its lanes.
 template <bool kCluster>
 __device__ inline bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where) {
@@ -243,26 +260,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; s++) {
-            mbar_init(&bars->full[s], CG);
+            mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 1);
             mbar_init(&bars->tail[s], 1);
+            mbar_init(&bars->peer[s], 1);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 4 * CG);
+            mbar_init(&bars->acc_empty[b], kEpiWarps * CG);
         }
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
         fence_barrier_init();
     }
-    if (warp == 6) tmem_alloc<CG>(&bars->tmem_slot);
-    if (warp == 4 && lane == 0) {
+    if (warp == kTailWarp) tmem_alloc<CG>(&bars->tmem_slot);
+    if (warp == kTmaWarp && lane == 0) {
         tma_prefetch_desc(&map_a);
         tma_prefetch_desc(&map_b);
     }
     {   // The groups' rows and row tiles, four groups a thread: offsets clamped into the
         // rows and to no less than those before them (a running maximum), then summed.
-        constexpr int kPer = NVFP4_MOE_MAX_GROUPS / kThreads;
+        constexpr int kPer = NVFP4_MOE_MAX_GROUPS / kScanThreads;
         const int E = q.p.groups, e0 = kPer * threadIdx.x;
         int off[kPer + 1], top = 0;
 #pragma unroll
@@ -319,29 +337,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == S) { stage = 0; phase ^= 1; }
     };
 
-    if (warp == 4) {
+    if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA
         uint32_t issued = 0, issued_phase = 0;   // stages loaded, and the parity of their last use
         bool ok = true;
         for (int i = cid; ok && i < tiles.total; i += ncl) {
             const OutTile t = tiles.at(i);
-            const int half = cdiv(t.nrow, 16 * CG) * 16;   // B columns of this CTA
-            const int brow = t.row0 + rank * half, acol = t.m0 + rank * 128;
-            const int nbox = MODE == kDw ? cdiv(half, 64) : cdiv(half, q.box);
-            const uint32_t bytes = kABytes + nbox * (MODE == kDw ? 64 : q.box) * kLine;
-            for (int c = 0; c < t.c; c += kStep) {
-                if (!warp_wait<CG == 2>(&bars->empty[stage], phase ^ 1, abort, 1)) { ok = false; break; }
-                if (lane == 0) {
+            if (lane == 0) {
+                const int half = cdiv(t.nrow, 16 * CG) * 16;   // B columns of this CTA
+                const int brow = t.row0 + rank * half, acol = t.m0 + rank * 128;
+                const int nbox = MODE == kDw ? cdiv(half, 64) : cdiv(half, q.box);
+                const uint32_t bytes = kABytes + nbox * (MODE == kDw ? 64 : q.box) * kLine;
+                for (int c = 0; c < t.c; c += kStep) {
+                    if (!mbar_wait<CG == 2>(&bars->empty[stage], phase ^ 1, abort, g_status, 1)) { ok = false; break; }
                     uint8_t *a = smem + stage * stage_size, *b = a + kABytes;
+                    // A stage whose last rows have to be zeroed is counted by each CTA for
+                    // itself first; every other one by the leader, for both.
                     const bool tail = MODE == kDw && t.c - c < kStep && ((t.c - c) & 15);
                     uint64_t *bar = tail ? &bars->tail[stage] : &bars->full[stage];
                     const uint32_t leader = CG == 1 ? 0 : mapa_shared(bar, tail ? rank : 0);
                     if (tail)
-                        mbar_arrive_expect_tx(bar, bytes);   // this CTA's own bytes
+                        mbar_arrive_expect_tx(bar, bytes);
                     else if (rank == 0)
                         mbar_arrive_expect_tx(bar, CG * bytes);
-                    else
-                        arrive_leader<CG>(bar);
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                     if (MODE == kFwd)
@@ -356,10 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             tma_3d<CG>(b + j * q.box * kLine, &map_b, bar, leader, c, brow + j * q.box, 0);
                     }
+                    next();
                 }
-                __syncwarp();
-                next();
             }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
         }
         // The last load of every stage has landed before the CTA ends (after a give-up
         // nobody else has waited for them).
@@ -367,25 +385,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 0; s < S; s++)
                 if (issued & (1u << s)) mbar_wait_drain(&bars->full[s], (issued_phase >> s) & 1, kDrainNs);
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------------ MMA (leader)
         if (rank == 0) {
             uint32_t acc_phase = 0, it = 0;
-            bool ok = true;
+            bool ok = true, ready = false;   // ready: the current stage has already been seen full
             for (int i = cid; ok && i < tiles.total; i += ncl) {
                 const OutTile t = tiles.at(i);
                 if (MODE == kDw && t.c == 0) continue;
                 const int buf = it++ & 1;
-                const uint32_t idesc = q.idesc | (uint32_t)(cdiv(t.nrow, 16 * CG) * 2 * CG) << 17;
-                if (!warp_wait<CG == 2>(&bars->acc_empty[buf], ((acc_phase >> buf) & 1) ^ 1, abort, 2)) break;
-                acc_phase ^= 1u << buf;
-                tc_fence_after();
-                const uint32_t d = tmem_base + buf * kAccCols;
-                for (int c = 0; c < t.c; c += kStep) {
-                    if (!warp_wait<CG == 2>(&bars->full[stage], phase, abort, 3)) { ok = false; break; }
+                if (lane == 0) {
+                    const uint32_t idesc = q.idesc | (uint32_t)(cdiv(t.nrow, 16 * CG) * 2 * CG) << 17;
+                    const uint32_t d = tmem_base + buf * kAccCols;
+                    ok = mbar_wait<CG == 2>(&bars->acc_empty[buf], ((acc_phase >> buf) & 1) ^ 1, abort, g_status, 2);
                     tc_fence_after();
-                    if (lane == 0) {
+                    for (int c = 0; ok && c < t.c; c += kStep) {
+                        if (!ready && !mbar_wait<CG == 2>(&bars->full[stage], phase, abort, g_status, 3)) { ok = false; break; }
+                        tc_fence_after();
                         const uint32_t a = smem_u32(smem + stage * stage_size), b = a + kABytes;
+                        uint64_t *empty = &bars->empty[stage];
+                        // the next stage is looked at while this one's MMAs go out
+                        next();
+                        ready = mbar_test<CG == 2>(&bars->full[stage], phase);
                         const uint64_t ad = MODE == kFwd ? smem_desc_sw128(a) : desc_mn(a);
                         const uint64_t bd = MODE == kDw ? desc_mn(b) : smem_desc_sw128(b);
                         // 32 bytes of K a step, or 16 rows of 128 bytes
@@ -394,13 +415,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int s = 0; s < 4; s++)
                             if (s < steps) mma<CG, kI8>(d, ad + s * kA, bd + s * kB, idesc, (c | s) != 0);
-                        commit<CG>(&bars->empty[stage]);
+                        commit<CG>(empty);
                     }
-                    __syncwarp();
-                    next();
+                    if (ok) commit<CG>(&bars->acc_full[buf]);
                 }
-                if (ok && lane == 0) commit<CG>(&bars->acc_full[buf]);
-                __syncwarp();
+                acc_phase ^= 1u << buf;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
             // every MMA this thread issued completes before TMEM is freed
             if (lane == 0) {
@@ -412,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
-    } else if (warp == 6) {
+    } else if (warp == kTailWarp) {
         // --------------------------------------- dw: zeroes a group's last rows
         if (MODE == kDw) {
             uint32_t tail_phase = 0;
@@ -424,7 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int left = t.c - (steps - 1) * kStep;   // rows of the last stage
                 if (t.c && (left & 15)) {
                     const int last = (stage + steps - 1) % S;
-                    if (!warp_wait<false>(&bars->tail[last], (tail_phase >> last) & 1, abort, 4)) break;
+                    const uint32_t parity = (tail_phase >> last) & 1;
+                    if (!warp_wait<false>(&bars->tail[last], parity, abort, 4)) break;
                     tail_phase ^= 1u << last;
                     uint8_t *a = smem + last * stage_size, *b = a + kABytes;
                     const int pad = 16 - (left & 15), nb = cdiv(half, 64);   // rows to zero, in each 64-column box
@@ -435,23 +456,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) arrive_leader<CG>(&bars->full[last]);
+                    // the leader's own rows and its peer's: one arrival for both
+                    if (CG == 2 && rank == 0 && !warp_wait<true>(&bars->peer[last], parity, abort, 6)) break;
+                    if (lane == 0) arrive_leader<CG>(rank == 0 ? &bars->full[last] : &bars->peer[last]);
                 }
                 stage = (stage + steps) % S;
             }
         }
-    } else if (warp < 4) {
+    } else if (warp < kEpiWarps) {
         // -------------------------------------------------------- epilogue
         uint32_t acc_phase = 0, it = 0;
         const int cols = MODE == kFwd ? q.p.n : q.p.k;
+        const int quarter = warp & 3, first = 32 * (warp >> 2);   // TMEM lanes; first of every 64 columns
         for (int i = cid; i < tiles.total; i += ncl) {
             const OutTile t = tiles.at(i);
-            const int col = t.m0 + rank * 128 + 32 * warp + lane;
+            const int col = t.m0 + rank * 128 + 32 * quarter + lane;
             const bool mine = col < cols;
             const bool none = MODE == kDw && t.c == 0;   // an expert without rows: zeros
             if (none && q.p.out_add) continue;
             const int64_t at = (MODE == kDw ? (int64_t)t.e * q.p.n + t.row0 : t.row0) * q.p.out_ld + col;
-            const float cs = kI8 && mine ? q.p.w_scale[(int64_t)t.e * q.p.n + col] : 1.0f;
+            // the scales come in while the sums are still being formed
+            float cs = 1.0f, rs[kAccCols / 64];
+            if (kI8) {
+                if (mine) cs = q.p.w_scale[(int64_t)t.e * q.p.n + col];
+#pragma unroll
+                for (int h = 0; h < kAccCols / 64; h++) {
+                    const int r = first + 64 * h + lane;
+                    rs[h] = r < t.nrow ? q.p.x_scale[t.row0 + r] : 0.0f;
+                }
+            }
             const int buf = it & 1;
             if (!none) {
                 it++;
@@ -459,9 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 acc_phase ^= 1u << buf;
                 tc_fence_after();
             }
-            const uint32_t tbase = tmem_base + buf * kAccCols + ((uint32_t)(warp * 32) << 16);
-#pragma unroll 1
-            for (int r = 0; r < t.nrow; r += 32) {
+            const uint32_t tbase = tmem_base + buf * kAccCols + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll
+            for (int h = 0; h < kAccCols / 64; h++) {
+                const int r = first + 64 * h;
+                if (r >= t.nrow) break;
                 float v[32];
                 const int n = min(32, t.nrow - r);
                 if (none) {
@@ -471,11 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t u[32];
                     __syncwarp();
                     tmem_ld32(tbase + r, u);
-                    const float rs = kI8 && lane < n ? q.p.x_scale[t.row0 + r + lane] : 0.0f;
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; j++)
-                        v[j] = kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs, j) * cs) : __uint_as_float(u[j]);
+                        v[j] = kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs[h], j) * cs) : __uint_as_float(u[j]);
                 }
                 if (mine) {
                     const int64_t o = at + r * q.p.out_ld;
@@ -505,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (CG == 2) cluster_sync_all();   // no MMA, copy or arrival of the pair touches either CTA past here
-    if (warp == 6) {
+    if (warp == kTailWarp) {
         tc_fence_after();
         tmem_dealloc<CG>(tmem_base);
     }
