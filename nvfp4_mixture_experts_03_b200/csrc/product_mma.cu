@@ -38,6 +38,7 @@ constexpr int kTmemCols = 2 * kAccCols;
 constexpr int kLine = 128;              // bytes of a stage's K (or M, N) extent: one swizzle row
 constexpr int kABytes = 128 * kLine;    // A: 128 rows (K-major) or 2 x 64 columns x 64 rows
 constexpr int kMaxStages = 10;
+constexpr int kBand = 8;                // row tiles of a band (Tiles::at)
 constexpr size_t kSmemLimit = 227 * 1024;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr uint64_t kSettleNs = 1000000ull;   // lets in-flight copies land after an abort
@@ -50,9 +51,15 @@ struct MmaParams {
     uint32_t idesc;        // instruction descriptor without its N
     int32_t out_type;
     int32_t bn;            // most rows of a tile (N); a multiple of 64 per CTA for dw
-    int32_t box;           // rows of one K-major B box
+    int32_t box;           // rows of the larger K-major B box
     int32_t stages;
+    int32_t staged;        // 16-bit outputs leave through shared memory (map_o is set)
+    int32_t a_whole, b_whole;   // M- or N-major operands: all of a stage's 64-column boxes as one
 };
+
+constexpr int kBoxSmall = 32;           // rows of the smaller K-major B box
+constexpr int kOutRows = 32;            // rows of an output box
+constexpr int kOutBytes = kOutRows * 128 * 2;   // its staging: 128 columns of 16 bits
 
 struct __align__(8) Bars {
     uint64_t full[kMaxStages];    // leader: its one arrival, and the bytes of every CTA of the group
@@ -76,7 +83,7 @@ struct Groups {
 
 inline size_t stage_bytes(int bn, int cg) { return kABytes + (size_t)bn / cg * kLine; }
 inline size_t smem_bytes(int bn, int cg, int stages) {
-    return 1024 + stages * stage_bytes(bn, cg) + sizeof(Bars) + sizeof(Groups);
+    return 1024 + stages * stage_bytes(bn, cg) + 2 * kOutBytes + sizeof(Bars) + sizeof(Groups);
 }
 
 template <int CG>
@@ -93,6 +100,43 @@ __device__ inline void tma_3d(void *dst, const CUtensorMap *map, uint64_t *bar, 
             " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
             "l"((uint64_t)map), "r"(bar_leader), "r"(x), "r"(y), "r"(z)
             : "memory");
+}
+
+// The same from a map whose columns are split into [blocks][64]: one copy for all of a
+// stage's 64-column boxes.
+template <int CG>
+__device__ inline void tma_4d(void *dst, const CUtensorMap *map, uint64_t *bar, uint32_t bar_leader, int block, int y, int z) {
+    if (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+                smem_u32(dst)),
+            "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(0), "r"(y), "r"(block), "r"(z)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+            "l"((uint64_t)map), "r"(bar_leader), "r"(0), "r"(y), "r"(block), "r"(z)
+            : "memory");
+}
+
+// Bulk tensor store of an output box, in this thread's bulk group.
+__device__ inline void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n cp.async.bulk.commit_group;" ::"l"(map),
+                 "r"(smem_u32(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+// Named barrier of the four epilogue warps that share a staging buffer.
+__device__ inline void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+
+__device__ inline bool half_all(int half, bool v) {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.and.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"(1 + half), "r"((uint32_t)v)
+                 : "memory");
+    return r != 0;
 }
 
 template <int CG, bool kI8>
@@ -190,16 +234,21 @@ template <int MODE, int CG>
 struct Tiles {
     const MmaParams &q;
     const Groups &g;
-    int mt, total;   // column tiles; all tiles
+    int mt, rt, total;   // column tiles, row tiles (dw: of all groups), all tiles
     __device__ Tiles(const MmaParams &q_, const Groups &g_) : q(q_), g(g_) {
         mt = cdiv(MODE == kFwd ? q.p.n : q.p.k, 128 * CG);
-        total = mt * (MODE == kDw ? q.p.groups * cdiv(q.p.n, q.bn) : g.before[q.p.groups]);
+        rt = MODE == kDw ? q.p.groups * cdiv(q.p.n, q.bn) : g.before[q.p.groups];
+        total = mt * rt;
     }
-    // Tile i, by a whole warp.
+    // Tile i, by a whole warp. Tiles run down kBand row tiles before they step to the next
+    // columns, so that those in flight at a time share both operands in L2: with whole
+    // rows of tiles instead, 8192 x 8192 x 4096 read its operands seven times from memory.
     __device__ OutTile at(int i) const {
         OutTile t;
-        const int r = i / mt, lane = threadIdx.x & 31;
-        t.m0 = (i - r * mt) * 128 * CG;
+        const int lane = threadIdx.x & 31;
+        const int band = i / (kBand * mt), j = i - band * kBand * mt, high = min(kBand, rt - band * kBand);
+        const int r = band * kBand + j % high;
+        t.m0 = j / high * 128 * CG;
         if (MODE == kDw) {
             const int nt = cdiv(q.p.n, q.bn);
             t.e = r / nt;
@@ -244,11 +293,13 @@ __device__ inline void store_rows(O *o, int64_t ld, const float (&v)[32], int nr
 template <int MODE, bool kI8, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     product_mma_kernel(const __grid_constant__ MmaParams q, const __grid_constant__ CUtensorMap map_a,
-                       const __grid_constant__ CUtensorMap map_b) {
+                       const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_b_small,
+                       const __grid_constant__ CUtensorMap map_o) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t b_bytes = (uint32_t)q.bn / CG * kLine, stage_size = kABytes + b_bytes;
-    Bars *bars = reinterpret_cast<Bars *>(smem + q.stages * stage_size);
+    uint8_t *out_stage = smem + q.stages * stage_size;
+    Bars *bars = reinterpret_cast<Bars *>(out_stage + 2 * kOutBytes);
     Groups *groups = reinterpret_cast<Groups *>(bars + 1);
     volatile int *abort = &bars->abort;
 
@@ -322,8 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (e0 + i <= E) groups->before[e0 + i] = upto;
             upto += tiles[i];
         }
-        // with the most groups the total has no thread of its own
-        if (e0 + kPer == E) groups->before[E] = upto;
     }
     tc_fence_before();
     __syncthreads();
@@ -346,8 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 const int half = cdiv(t.nrow, 16 * CG) * 16;   // B columns of this CTA
                 const int brow = t.row0 + rank * half, acol = t.m0 + rank * 128;
-                const int nbox = MODE == kDw ? cdiv(half, 64) : cdiv(half, q.box);
-                const uint32_t bytes = kABytes + nbox * (MODE == kDw ? 64 : q.box) * kLine;
+                // A copy costs the TMA unit much the same whatever its rows: few and large ones
+                // (one box of 128 rows instead of four of 32: 435 -> 373 us for 8192 x 8192 x
+                // 4096), small ones where the tile has few rows.
+                const bool few = half <= 2 * kBoxSmall;
+                const int box = MODE == kDw ? 64 : few ? kBoxSmall : q.box;
+                const int nbox = MODE == kDw ? q.b_whole ? q.bn / CG / 64 : cdiv(half, 64) : cdiv(half, box);
+                const CUtensorMap *mb = MODE != kDw && few ? &map_b_small : &map_b;
+                const uint32_t bytes = kABytes + nbox * box * kLine;
                 for (int c = 0; c < t.c; c += kStep) {
                     if (!mbar_wait<CG == 2>(&bars->empty[stage], phase ^ 1, abort, g_status, 1)) { ok = false; break; }
                     uint8_t *a = smem + stage * stage_size, *b = a + kABytes;
@@ -362,18 +417,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive_expect_tx(bar, CG * bytes);
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    const int z = MODE == kDw ? 0 : t.e;
                     if (MODE == kFwd)
-                        tma_3d<CG>(a, &map_a, bar, leader, c, acol, t.e);
-                    else {
+                        tma_3d<CG>(a, &map_a, bar, leader, c, acol, z);
+                    else if (q.a_whole)
+                        tma_4d<CG>(a, &map_a, bar, leader, acol / 64, t.c0 + c, z);
+                    else
                         for (int h = 0; h < 2; h++)
-                            tma_3d<CG>(a + h * 64 * kLine, &map_a, bar, leader, acol + 64 * h, t.c0 + c, MODE == kDx ? t.e : 0);
-                    }
-                    for (int j = 0; j < nbox; j++) {
-                        if (MODE == kDw)
-                            tma_3d<CG>(b + j * 64 * kLine, &map_b, bar, leader, brow + 64 * j, t.c0 + c, 0);
-                        else
-                            tma_3d<CG>(b + j * q.box * kLine, &map_b, bar, leader, c, brow + j * q.box, 0);
-                    }
+                            tma_3d<CG>(a + h * 64 * kLine, &map_a, bar, leader, acol + 64 * h, t.c0 + c, z);
+                    if (MODE == kDw && q.b_whole)
+                        tma_4d<CG>(b, &map_b, bar, leader, brow / 64, t.c0 + c, 0);
+                    else
+                        for (int j = 0; j < nbox; j++) {
+                            if (MODE == kDw)
+                                tma_3d<CG>(b + j * 64 * kLine, mb, bar, leader, brow + 64 * j, t.c0 + c, 0);
+                            else
+                                tma_3d<CG>(b + j * box * kLine, mb, bar, leader, c, brow + j * box, 0);
+                        }
                     next();
                 }
             }
@@ -488,7 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int buf = it & 1;
             if (!none) {
                 it++;
-                if (!warp_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, 5)) break;
+                // the four warps that share a staging buffer leave together, or not at all
+                if (!half_all(warp >> 2, mbar_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, g_status, 5))) break;
                 acc_phase ^= 1u << buf;
                 tc_fence_after();
             }
@@ -511,7 +572,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; j++)
                         v[j] = kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs[h], j) * cs) : __uint_as_float(u[j]);
                 }
-                if (mine) {
+                if (q.staged && n == kOutRows) {
+                    // 32 rows x this CTA's 128 columns by one copy: 256 bytes of each row at a
+                    // time instead of the 64 that a warp has
+                    const int half = warp >> 2;
+                    uint16_t *os = reinterpret_cast<uint16_t *>(out_stage + half * kOutBytes) + 32 * quarter + lane;
+                    if (quarter == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    half_sync(half);
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        os[j * 128] = q.out_type == NVFP4_MOE_TYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v[j]))
+                                                                        : __half_as_ushort(__float2half_rn(v[j]));
+                    fence_proxy_async_smem();
+                    half_sync(half);
+                    if (quarter == 0 && lane == 0 && t.m0 + rank * 128 < cols)
+                        tma_store_2d(&map_o, out_stage + half * kOutBytes, t.m0 + rank * 128,
+                                     (MODE == kDw ? t.e * q.p.n : 0) + t.row0 + r);
+                } else if (mine) {
                     const int64_t o = at + r * q.p.out_ld;
                     if (q.out_type == NVFP4_MOE_TYPE_F32)
                         store_rows(static_cast<float *>(q.p.out) + o, q.p.out_ld, v, n, q.p.out_add);
@@ -527,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) arrive_leader<CG>(&bars->acc_empty[buf]);
             }
         }
+        if (quarter == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     __syncwarp();
@@ -547,23 +625,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------- host
 
-// [matrices][rows][cols], 128-byte x box_rows boxes in the 128-byte swizzle, zeros outside.
-bool make_map(CUtensorMap *m, const void *base, nvfp4_moe_type type, int64_t cols, int64_t rows, int64_t matrices, int64_t ld,
-              int box_rows) {
+struct Operand {
+    const void *base;
+    int64_t cols, rows, matrices, ld;   // [matrices][rows][cols], row stride in elements
+};
+
+CUtensorMapDataType map_type(nvfp4_moe_type t) {
+    return t == NVFP4_MOE_TYPE_INT8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+           : t == NVFP4_MOE_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+}
+
+// Boxes of 128 bytes x `rows` rows in the 128-byte swizzle, zeros outside. blocks > 0: the
+// columns as [blocks of 64][64], that many of them to a box (cols a multiple of 64: past
+// the last block there is nothing, within it no column is out of range).
+bool map_operand(CUtensorMap *m, const Operand &o, nvfp4_moe_type type, int rows, int blocks) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const int es = type == NVFP4_MOE_TYPE_INT8 ? 1 : 2;
-    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)matrices};
-    const cuuint64_t strides[2] = {(cuuint64_t)(ld * es), (cuuint64_t)(ld * es * (matrices > 1 ? rows : 1))};
-    const cuuint32_t box[3] = {(cuuint32_t)(kLine / es), (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
-    const CUtensorMapDataType dt = type == NVFP4_MOE_TYPE_INT8  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : type == NVFP4_MOE_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return fn(m, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t row = (cuuint64_t)(o.ld * es), matrix = (cuuint64_t)(o.ld * es * (o.matrices > 1 ? o.rows : 1));
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    if (blocks) {
+        const cuuint64_t dims[4] = {64, (cuuint64_t)o.rows, (cuuint64_t)(o.cols / 64), (cuuint64_t)o.matrices};
+        const cuuint64_t strides[3] = {row, kLine, matrix};
+        const cuuint32_t box[4] = {64, (cuuint32_t)rows, (cuuint32_t)blocks, 1};
+        return fn(m, map_type(type), 4, const_cast<void *>(o.base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+               CUDA_SUCCESS;
+    }
+    const cuuint64_t dims[3] = {(cuuint64_t)o.cols, (cuuint64_t)o.rows, (cuuint64_t)o.matrices};
+    const cuuint64_t strides[2] = {row, matrix};
+    const cuuint32_t box[3] = {(cuuint32_t)(kLine / es), (cuuint32_t)rows, 1};
+    return fn(m, map_type(type), 3, const_cast<void *>(o.base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
 }
 
-typedef void (*MmaKernel)(const MmaParams, const CUtensorMap, const CUtensorMap);
+// 16-bit output rows as a store target: boxes of 128 columns x kOutRows rows.
+bool map_output(CUtensorMap *m, void *base, nvfp4_moe_type type, int64_t rows, int64_t cols, int64_t ld) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(ld * 2)};
+    const cuuint32_t box[2] = {128, kOutRows}, ones[2] = {1, 1};
+    return fn(m, map_type(type), 2, base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+typedef void (*MmaKernel)(const MmaParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap);
 
 MmaKernel kernel_of(int mode, bool i8, int cg) {
     if (i8) return cg == 1 ? product_mma_kernel<kFwd, true, 1> : product_mma_kernel<kFwd, true, 2>;
@@ -640,21 +748,25 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     const int avg = mode == kDw ? p.n : cdiv(p.rows, p.groups);
     const int cg = avg >= 256 && cols > 128 ? 2 : 1;
     q.bn = cg == 2 ? 256 : avg >= 128 ? 256 : avg > 32 || mode == kDw ? 128 : 64;
-    q.box = 32;
+    q.box = std::min(128, q.bn / cg);
     q.stages = (int)std::min<size_t>(kMaxStages, (kSmemLimit - smem_bytes(q.bn, cg, 0)) / stage_bytes(q.bn, cg));
     // D F32 (or S32), A and B F16, BF16 or S8, their majors, M
     q.idesc = i8 ? (2u << 4) | (1u << 7) | (1u << 10) : (1u << 4) | (type == NVFP4_MOE_TYPE_BF16 ? (1u << 7) | (1u << 10) : 0u);
     if (mode != kFwd) q.idesc |= 1u << 15;
     if (mode == kDw) q.idesc |= 1u << 16;
     q.idesc |= (uint32_t)(128 * cg >> 4) << 24;
-    CUtensorMap a, b;
-    bool ok;
-    if (mode == kFwd)
-        ok = make_map(&a, p.w, type, p.k, p.n, p.groups, p.w_ld, 128) && make_map(&b, p.x, type, p.k, p.rows, 1, p.x_ld, q.box);
-    else if (mode == kDx)
-        ok = make_map(&a, p.w, type, p.k, p.n, p.groups, p.w_ld, 64) && make_map(&b, p.dy, type, p.n, p.rows, 1, p.dy_ld, q.box);
-    else
-        ok = make_map(&a, p.x, type, p.k, p.rows, 1, p.x_ld, 64) && make_map(&b, p.dy, type, p.n, p.rows, 1, p.dy_ld, 64);
+    const Operand w{p.w, p.k, p.n, p.groups, p.w_ld}, x{p.x, p.k, p.rows, 1, p.x_ld}, dy{p.dy, p.n, p.rows, 1, p.dy_ld};
+    const Operand &oa = mode == kDw ? x : w, &ob = mode == kFwd ? x : dy;
+    q.a_whole = mode != kFwd && oa.cols % 64 == 0;
+    q.b_whole = mode == kDw && ob.cols % 64 == 0 && p.n % (64 * cg) == 0;
+    const int64_t out_rows = mode == kDw ? (int64_t)p.groups * p.n : p.rows;
+    q.staged = out != NVFP4_MOE_TYPE_F32 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.out_ld % 8 == 0;
+    CUtensorMap a, b, b_small, o;
+    bool ok = map_operand(&a, oa, type, mode == kFwd ? 128 : 64, q.a_whole ? 2 : 0) &&
+              map_operand(&b, ob, type, mode == kDw ? 64 : q.box, q.b_whole ? q.bn / cg / 64 : 0);
+    b_small = o = b;   // where they are not used
+    if (ok && mode != kDw) ok = map_operand(&b_small, ob, type, kBoxSmall, 0);
+    if (ok && q.staged) ok = map_output(&o, p.out, out, out_rows, cols, p.out_ld);
     if (!ok) return cudaErrorInvalidValue;
     // no more CTAs than there can be tiles
     const int64_t mt = cdiv(cols, 128 * cg);
@@ -663,7 +775,7 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     const int units = (int)std::min<int64_t>(cg == 2 ? r.pairs : r.ctas, std::max<int64_t>(most, 1));
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(units * cg, cg, smem_bytes(q.bn, cg, q.stages), s, &attr);
-    return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg), q, a, b);
+    return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg), q, a, b, b_small, o);
 }
 
 int product_status(cudaStream_t s) {
