@@ -30,13 +30,14 @@ namespace nvmoe {
 namespace {
 
 constexpr int kEpiWarps = 8;            // two for each quarter of the TMEM lanes
-constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kTailWarp = kEpiWarps + 2;
+constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kTailWarp = kEpiWarps + 2, kTileWarp = kEpiWarps + 3;
 constexpr int kThreads = 32 * (kEpiWarps + 4);
 constexpr int kScanThreads = 256;       // of the CTA's, list the groups
 constexpr int kAccCols = 256;           // two accumulators of up to 256 columns
 constexpr int kTmemCols = 2 * kAccCols;
 constexpr int kLine = 128;              // bytes of a stage's K (or M, N) extent: one swizzle row
 constexpr int kABytes = 128 * kLine;    // A: 128 rows (K-major) or 2 x 64 columns x 64 rows
+constexpr int kTilesAhead = 4;          // tiles that the tile warp lists ahead
 constexpr int kMaxStages = 10;
 constexpr int kBand = 8;                // row tiles of a band (Tiles::at)
 constexpr size_t kSmemLimit = 227 * 1024;
@@ -61,20 +62,32 @@ constexpr int kBoxSmall = 32;           // rows of the smaller K-major B box
 constexpr int kOutRows = 32;            // rows of an output box
 constexpr int kOutBytes = kOutRows * 128 * 2;   // its staging: 128 columns of 16 bits
 
-struct __align__(8) Bars {
+struct __align__(16) Bars {
     uint64_t full[kMaxStages];    // leader: its one arrival, and the bytes of every CTA of the group
     uint64_t empty[kMaxStages];   // each CTA: the MMAs' commit
     uint64_t tail[kMaxStages];    // dw, each CTA: its own bytes of a stage with rows to zero
     uint64_t peer[kMaxStages];    // dw, leader: the other CTA has zeroed its rows of a stage
     uint64_t acc_full[2];         // each CTA: the MMAs' commit
     uint64_t acc_empty[2];        // leader: the epilogue warps of each CTA
+    uint64_t tile_full[kTilesAhead];    // the tile warp's entry
+    uint64_t tile_empty[kTilesAhead];   // the warps that have read it
     uint64_t drain;
     uint32_t tmem_slot;
     int abort;
 };
 
-// The groups' rows, and the number of row tiles before each.
+struct __align__(16) OutTile {
+    int32_t e;       // group, or -1 past the last tile
+    int32_t m0;      // first output column
+    int32_t row0;    // first output row: of all rows (product, dx), of the group's matrix (dw)
+    int32_t nrow;    // output rows of the tile (1..bn)
+    int32_t c0, c;   // the summed index: first and count (dw: the group's rows)
+    int32_t pad[2];
+};
+
+// The groups' rows, and the number of row tiles before each; the tiles listed ahead.
 struct Groups {
+    OutTile ahead[kTilesAhead];
     int32_t lo[NVFP4_MOE_MAX_GROUPS];
     int32_t count[NVFP4_MOE_MAX_GROUPS];
     int32_t before[NVFP4_MOE_MAX_GROUPS + 1];
@@ -125,6 +138,33 @@ __device__ inline void tma_store_2d(const CUtensorMap *map, const void *src, int
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n cp.async.bulk.commit_group;" ::"l"(map),
                  "r"(smem_u32(src)), "r"(x), "r"(y)
                  : "memory");
+}
+
+// 16 lanes x 32 columns as fragments: registers 4i..4i+3 hold, of columns 8i + 2 (lane % 4)
+// and the one after it, lane row lane / 4 and then row lane / 4 + 8.
+__device__ inline void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Four 8 x 8 matrices of 16 bits, transposed on the way: lane l gives the address of row
+// l % 8 (16 bytes) of matrix l / 8.
+__device__ inline void stmatrix_trans(void *row, const uint32_t (&w)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(row)), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+
+__device__ inline uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ inline uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 // Named barrier of the four epilogue warps that share a staging buffer.
@@ -222,14 +262,6 @@ __device__ inline bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *a
     return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, abort, g_status, where));
 }
 
-struct OutTile {
-    int32_t e;       // group
-    int32_t m0;      // first output column
-    int32_t row0;    // first output row: of all rows (product, dx), of the group's matrix (dw)
-    int32_t nrow;    // output rows of the tile (1..bn)
-    int32_t c0, c;   // the summed index: first and count (dw: the group's rows)
-};
-
 template <int MODE, int CG>
 struct Tiles {
     const MmaParams &q;
@@ -320,6 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->acc_full[b], 1);
             mbar_init(&bars->acc_empty[b], kEpiWarps * CG);
         }
+        // read by the TMA warp, the leader's MMA warp, dw's tail warp and the epilogue
+        for (int a = 0; a < kTilesAhead; a++) {
+            mbar_init(&bars->tile_full[a], 1);
+            mbar_init(&bars->tile_empty[a], 1 + (rank == 0) + (MODE == kDw) + kEpiWarps);
+        }
         mbar_init(&bars->drain, 1);
         bars->abort = 0;
         fence_barrier_init();
@@ -379,7 +416,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (CG == 2) cluster_sync_all();   // both CTAs' barriers initialised and TMEM allocated
     tc_fence_after();
     const uint32_t tmem_base = bars->tmem_slot;
-    const Tiles<MODE, CG> tiles(q, *groups);
+    // The next tile, listed by the tile warp (finding it takes a few integer divisions: about
+    // a thousand cycles that no other warp should spend between two tiles). e is -1 past
+    // the last one, and after a wait that gave up.
+    int slot = 0;
+    uint32_t slot_phase = 0;
+    auto next_tile = [&]() {
+        OutTile t;
+        t.e = -1;
+        if (warp_wait<false>(&bars->tile_full[slot], slot_phase, abort, 7)) {
+            t = groups->ahead[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->tile_empty[slot]);
+            if (++slot == kTilesAhead) { slot = 0; slot_phase ^= 1; }
+        }
+        return t;
+    };
     int stage = 0;
     uint32_t phase = 0;
     auto next = [&]() {
@@ -390,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ TMA
         uint32_t issued = 0, issued_phase = 0;   // stages loaded, and the parity of their last use
         bool ok = true;
-        for (int i = cid; ok && i < tiles.total; i += ncl) {
-            const OutTile t = tiles.at(i);
+        while (ok) {
+            const OutTile t = next_tile();
+            if (t.e < 0) break;
             if (lane == 0) {
                 const int half = cdiv(t.nrow, 16 * CG) * 16;   // B columns of this CTA
                 const int brow = t.row0 + rank * half, acol = t.m0 + rank * 128;
@@ -450,8 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             uint32_t acc_phase = 0, it = 0;
             bool ok = true, ready = false;   // ready: the current stage has already been seen full
-            for (int i = cid; ok && i < tiles.total; i += ncl) {
-                const OutTile t = tiles.at(i);
+            while (ok) {
+                const OutTile t = next_tile();
+                if (t.e < 0) break;
                 if (MODE == kDw && t.c == 0) continue;
                 const int buf = it++ & 1;
                 if (lane == 0) {
@@ -496,9 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // --------------------------------------- dw: zeroes a group's last rows
         if (MODE == kDw) {
             uint32_t tail_phase = 0;
-            bool ok = true;
-            for (int i = cid; ok && i < tiles.total; i += ncl) {
-                const OutTile t = tiles.at(i);
+            while (true) {
+                const OutTile t = next_tile();
+                if (t.e < 0) break;
                 const int half = cdiv(t.nrow, 16 * CG) * 16;
                 const int steps = cdiv(t.c, kStep);
                 const int left = t.c - (steps - 1) * kStep;   // rows of the last stage
@@ -523,32 +577,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                 stage = (stage + steps) % S;
             }
         }
+    } else if (warp == kTileWarp) {
+        // ---------------------------------------------------- lists the tiles
+        const Tiles<MODE, CG> tiles(q, *groups);
+        for (int i = cid; ; i += ncl) {
+            OutTile t;
+            t.e = -1;
+            if (i < tiles.total) t = tiles.at(i);
+            if (!warp_wait<false>(&bars->tile_empty[slot], slot_phase ^ 1, abort, 8)) break;
+            if (lane == 0) {
+                groups->ahead[slot] = t;
+                mbar_arrive(&bars->tile_full[slot]);
+            }
+            __syncwarp();
+            if (++slot == kTilesAhead) { slot = 0; slot_phase ^= 1; }
+            if (t.e < 0) break;
+        }
     } else if (warp < kEpiWarps) {
         // -------------------------------------------------------- epilogue
         uint32_t acc_phase = 0, it = 0;
         const int cols = MODE == kFwd ? q.p.n : q.p.k;
         const int quarter = warp & 3, first = 32 * (warp >> 2);   // TMEM lanes; first of every 64 columns
-        for (int i = cid; i < tiles.total; i += ncl) {
-            const OutTile t = tiles.at(i);
+        while (true) {
+            const OutTile t = next_tile();
+            // the four warps that share a staging buffer leave together, or not at all
+            if (!half_all(warp >> 2, t.e >= 0)) break;
             const int col = t.m0 + rank * 128 + 32 * quarter + lane;
             const bool mine = col < cols;
             const bool none = MODE == kDw && t.c == 0;   // an expert without rows: zeros
             if (none && q.p.out_add) continue;
             const int64_t at = (MODE == kDw ? (int64_t)t.e * q.p.n + t.row0 : t.row0) * q.p.out_ld + col;
-            // the scales come in while the sums are still being formed
-            float cs = 1.0f, rs[kAccCols / 64];
+            // Scales of int8 products come in while the sums are still being formed: of this
+            // lane's column and rows, or of the rows and columns that a fragment gives it.
+            float cs = 1.0f, rs[kAccCols / 64], fcs[4], frs[kAccCols / 64][8];
             if (kI8) {
-                if (mine) cs = q.p.w_scale[(int64_t)t.e * q.p.n + col];
+                const float *ws = q.p.w_scale + (int64_t)t.e * q.p.n, *xs = q.p.x_scale + t.row0;
+                if (q.staged) {
+#pragma unroll
+                    for (int j = 0; j < 4; j++) fcs[j] = ws[min(col - lane + 8 * j + (lane >> 2), cols - 1)];
+                } else if (mine)
+                    cs = ws[col];
 #pragma unroll
                 for (int h = 0; h < kAccCols / 64; h++) {
-                    const int r = first + 64 * h + lane;
-                    rs[h] = r < t.nrow ? q.p.x_scale[t.row0 + r] : 0.0f;
+                    const int r = first + 64 * h;
+                    if (r >= t.nrow) break;
+                    if (q.staged) {
+#pragma unroll
+                        for (int j = 0; j < 8; j++) frs[h][j] = xs[min(r + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1), t.nrow - 1)];
+                    } else
+                        rs[h] = r + lane < t.nrow ? xs[r + lane] : 0.0f;
                 }
             }
             const int buf = it & 1;
             if (!none) {
                 it++;
-                // the four warps that share a staging buffer leave together, or not at all
                 if (!half_all(warp >> 2, mbar_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, g_status, 5))) break;
                 acc_phase ^= 1u << buf;
                 tc_fence_after();
@@ -558,8 +640,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < kAccCols / 64; h++) {
                 const int r = first + 64 * h;
                 if (r >= t.nrow) break;
-                float v[32];
                 const int n = min(32, t.nrow - r);
+                if (q.staged) {
+                    // 16 bits: fragments of 16 lanes x 8 columns hold two rows' values of a
+                    // column to a thread, which is what a transposing matrix store takes: 32
+                    // rows x 128 columns are staged by four of them a warp and leave as whole
+                    // boxes (two of 64 columns), or, at a group's end, in 16-byte pieces. Shared
+                    // memory is what the MMAs run on (each stage's bytes pass it twice in the
+                    // time of its MMAs), so what counts here is how few passes this takes.
+                    const int half = warp >> 2;
+                    uint8_t *os = out_stage + half * kOutBytes;
+                    uint32_t f[2][16];
+                    __syncwarp();
+                    if (!none) {
+                        tmem_ld_frag(tbase + r, f[0]);
+                        tmem_ld_frag(tbase + (16u << 16) + r, f[1]);
+                        tmem_ld_wait();
+                    }
+                    uint32_t w[4][4];   // [8 rows][8 columns], two rows to a word
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const uint32_t u0 = f[j >> 1][4 * i + 2 * (j & 1)], u1 = f[j >> 1][4 * i + 2 * (j & 1) + 1];
+                            float v0 = __uint_as_float(u0), v1 = __uint_as_float(u1);
+                            if (kI8) {
+                                v0 = (float)(int32_t)u0 * (frs[h][2 * i] * fcs[j]);
+                                v1 = (float)(int32_t)u1 * (frs[h][2 * i + 1] * fcs[j]);
+                            }
+                            w[i][j] = none ? 0u : q.out_type == NVFP4_MOE_TYPE_BF16 ? pack_bf16(v0, v1) : pack_f16(v0, v1);
+                        }
+                    if (quarter == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    half_sync(half);   // the previous chunk has left
+                    const int piece = 4 * quarter + (lane >> 3), k = lane & 7;
+                    uint8_t *to = os + (piece >> 3) * (kOutBytes / 2) + k * 128 + (((piece & 7) ^ k) << 4);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) stmatrix_trans(to + i * 8 * 128, w[i]);
+                    const int ocol = t.m0 + rank * 128, orow = (MODE == kDw ? t.e * q.p.n : 0) + t.row0 + r;
+                    if (n == kOutRows) {
+                        fence_proxy_async_smem();
+                        half_sync(half);
+                        if (quarter == 0 && lane == 0)
+                            for (int b = 0; b < 2; b++)
+                                if (ocol + 64 * b < cols) tma_store_2d(&map_o, os + b * (kOutBytes / 2), ocol + 64 * b, orow);
+                    } else {
+                        half_sync(half);
+                        for (int i = 32 * quarter + lane; i < n * 16; i += 128) {
+                            const int row = i >> 4, pc = i & 15, c0 = ocol + 8 * pc;
+                            const uint4 v = *reinterpret_cast<const uint4 *>(os + (pc >> 3) * (kOutBytes / 2) + row * 128 +
+                                                                             (((pc & 7) ^ (row & 7)) << 4));
+                            uint16_t *o = static_cast<uint16_t *>(q.p.out) + (int64_t)(orow + row) * q.p.out_ld + c0;
+                            if (c0 + 8 <= cols)
+                                *reinterpret_cast<uint4 *>(o) = v;
+                            else
+                                for (int c = 0; c < 8; c++)
+                                    if (c0 + c < cols) o[c] = (uint16_t)((c & 1 ? (&v.x)[c >> 1] >> 16 : (&v.x)[c >> 1]) & 0xffff);
+                        }
+                    }
+                    continue;
+                }
+                float v[32];
                 if (none) {
 #pragma unroll
                     for (int j = 0; j < 32; j++) v[j] = 0.0f;
@@ -572,23 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; j++)
                         v[j] = kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs[h], j) * cs) : __uint_as_float(u[j]);
                 }
-                if (q.staged && n == kOutRows) {
-                    // 32 rows x this CTA's 128 columns by one copy: 256 bytes of each row at a
-                    // time instead of the 64 that a warp has
-                    const int half = warp >> 2;
-                    uint16_t *os = reinterpret_cast<uint16_t *>(out_stage + half * kOutBytes) + 32 * quarter + lane;
-                    if (quarter == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    half_sync(half);
-#pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        os[j * 128] = q.out_type == NVFP4_MOE_TYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v[j]))
-                                                                        : __half_as_ushort(__float2half_rn(v[j]));
-                    fence_proxy_async_smem();
-                    half_sync(half);
-                    if (quarter == 0 && lane == 0 && t.m0 + rank * 128 < cols)
-                        tma_store_2d(&map_o, out_stage + half * kOutBytes, t.m0 + rank * 128,
-                                     (MODE == kDw ? t.e * q.p.n : 0) + t.row0 + r);
-                } else if (mine) {
+                if (mine) {
                     const int64_t o = at + r * q.p.out_ld;
                     if (q.out_type == NVFP4_MOE_TYPE_F32)
                         store_rows(static_cast<float *>(q.p.out) + o, q.p.out_ld, v, n, q.p.out_add);
@@ -661,13 +785,13 @@ bool map_operand(CUtensorMap *m, const Operand &o, nvfp4_moe_type type, int rows
            CUDA_SUCCESS;
 }
 
-// 16-bit output rows as a store target: boxes of 128 columns x kOutRows rows.
+// 16-bit output rows as a store target: boxes of 64 columns x kOutRows rows in the 128-byte swizzle.
 bool map_output(CUtensorMap *m, void *base, nvfp4_moe_type type, int64_t rows, int64_t cols, int64_t ld) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(ld * 2)};
-    const cuuint32_t box[2] = {128, kOutRows}, ones[2] = {1, 1};
-    return fn(m, map_type(type), 2, base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+    const cuuint32_t box[2] = {64, kOutRows}, ones[2] = {1, 1};
+    return fn(m, map_type(type), 2, base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
