@@ -54,13 +54,12 @@ struct MmaParams {
     int32_t bn;            // most rows of a tile (N); a multiple of 64 per CTA for dw
     int32_t box;           // rows of the larger K-major B box
     int32_t stages;
-    int32_t staged;        // 16-bit outputs leave through shared memory (map_o is set)
+    int32_t staged;        // whole batches of outputs leave as boxes (map_o is set); rows are 16-byte aligned
     int32_t a_whole, b_whole;   // M- or N-major operands: all of a stage's 64-column boxes as one
 };
 
 constexpr int kBoxSmall = 32;           // rows of the smaller K-major B box
-constexpr int kOutRows = 32;            // rows of an output box
-constexpr int kOutBytes = kOutRows * 128 * 2;   // its staging: 128 columns of 16 bits
+constexpr int kOutBytes = 16 * 1024;    // a half's staged outputs: 64 rows x 128 columns of 16 bits, 32 of 32
 
 struct __align__(16) Bars {
     uint64_t full[kMaxStages];    // leader: its one arrival, and the bytes of every CTA of the group
@@ -88,8 +87,7 @@ struct __align__(16) OutTile {
 // The groups' rows, and the number of row tiles before each; the tiles listed ahead.
 struct Groups {
     OutTile ahead[kTilesAhead];
-    int32_t lo[NVFP4_MOE_MAX_GROUPS];
-    int32_t count[NVFP4_MOE_MAX_GROUPS];
+    int32_t lo[NVFP4_MOE_MAX_GROUPS + 1];   // first row, and the last group's end
     int32_t before[NVFP4_MOE_MAX_GROUPS + 1];
     int32_t warp_sum[kThreads / 32], warp_max[kThreads / 32];
 };
@@ -133,9 +131,9 @@ __device__ inline void tma_4d(void *dst, const CUtensorMap *map, uint64_t *bar, 
             : "memory");
 }
 
-// Bulk tensor store of an output box, in this thread's bulk group.
+// Bulk tensor store of an output box.
 __device__ inline void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n cp.async.bulk.commit_group;" ::"l"(map),
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
                  "r"(smem_u32(src)), "r"(x), "r"(y)
                  : "memory");
 }
@@ -166,6 +164,8 @@ __device__ inline uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
+
+__device__ inline void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Named barrier of the four epilogue warps that share a staging buffer.
 __device__ inline void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
@@ -287,7 +287,7 @@ struct Tiles {
             t.row0 = (r - t.e * nt) * q.bn;
             t.nrow = min(q.bn, q.p.n - t.row0);
             t.c0 = g.lo[t.e];
-            t.c = g.count[t.e];
+            t.c = g.lo[t.e + 1] - t.c0;
         } else {
             // the last group with before[e] <= r: first among every 32nd, then among 32
             const int E = q.p.groups;
@@ -295,7 +295,7 @@ struct Tiles {
             const int c = 32 * hi + lane;
             t.e = 32 * hi + __popc(__ballot_sync(0xffffffffu, c < E && g.before[min(c, E)] <= r)) - 1;
             // the group's rows in equal tiles, whole multiples of 16 per CTA
-            const int n = g.before[t.e + 1] - g.before[t.e], cnt = g.count[t.e];
+            const int n = g.before[t.e + 1] - g.before[t.e], cnt = g.lo[t.e + 1] - g.lo[t.e];
             const int each = cdiv(cdiv(cnt, n), 16 * CG) * 16 * CG, first = (r - g.before[t.e]) * each;
             t.row0 = g.lo[t.e] + first;
             t.nrow = max(0, min(each, cnt - first));
@@ -306,23 +306,7 @@ struct Tiles {
     }
 };
 
-template <typename O>
-__device__ inline void store_rows(O *o, int64_t ld, const float (&v)[32], int nrow, bool add) {
-    if (add) {
-        float b[32];
-#pragma unroll
-        for (int j = 0; j < 32; j++) b[j] = j < nrow ? to_f32(o[j * ld]) : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 32; j++)
-            if (j < nrow) o[j * ld] = from_f32<O>(v[j] + b[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; j++)
-            if (j < nrow) o[j * ld] = from_f32<O>(v[j]);
-    }
-}
-
-template <int MODE, bool kI8, int CG>
+template <int MODE, bool kI8, int CG, bool kF32>
 __global__ void __launch_bounds__(kThreads, 1)
     product_mma_kernel(const __grid_constant__ MmaParams q, const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_b_small,
@@ -388,10 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kPer; i++) {
             run = max(run, off[i]);
             const int count = max(off[i + 1] - run, 0);
-            if (e0 + i < E) {
-                groups->lo[e0 + i] = run;
-                groups->count[e0 + i] = count;
-            }
+            if (e0 + i <= E) groups->lo[e0 + i] = run;
             tiles[i] = e0 + i < E ? cdiv(count, q.bn) : 0;
             sum += tiles[i];
         }
@@ -595,140 +576,166 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kEpiWarps) {
         // -------------------------------------------------------- epilogue
+        // The eight warps are two halves of four, one warp of each to a quarter of the TMEM
+        // lanes (32 output columns); the halves take batches of kBatch output rows in turn,
+        // each with a staging buffer of its own. Shared memory is what the MMAs run on (each
+        // stage's bytes pass it twice in the time of its MMAs) and a short sum leaves little
+        // time between two tiles, so what counts is how few passes and waits a batch takes.
+        constexpr int kBatch = kF32 ? 32 : 64, kBatches = kAccCols / (2 * kBatch);
         uint32_t acc_phase = 0, it = 0;
         const int cols = MODE == kFwd ? q.p.n : q.p.k;
-        const int quarter = warp & 3, first = 32 * (warp >> 2);   // TMEM lanes; first of every 64 columns
+        const int quarter = warp & 3, half = warp >> 2;
+        const bool storer = quarter == 0 && lane == 0;   // issues this half's bulk stores
+        uint8_t *os = out_stage + half * kOutBytes;
         while (true) {
             const OutTile t = next_tile();
             // the four warps that share a staging buffer leave together, or not at all
-            if (!half_all(warp >> 2, t.e >= 0)) break;
-            const int col = t.m0 + rank * 128 + 32 * quarter + lane;
-            const bool mine = col < cols;
+            if (!half_all(half, t.e >= 0)) break;
             const bool none = MODE == kDw && t.c == 0;   // an expert without rows: zeros
             if (none && q.p.out_add) continue;
-            const int64_t at = (MODE == kDw ? (int64_t)t.e * q.p.n + t.row0 : t.row0) * q.p.out_ld + col;
-            // Scales of int8 products come in while the sums are still being formed: of this
-            // lane's column and rows, or of the rows and columns that a fragment gives it.
-            float cs = 1.0f, rs[kAccCols / 64], fcs[4], frs[kAccCols / 64][8];
+            const int col0 = t.m0 + rank * 128, col = col0 + 32 * quarter + lane;   // of the CTA, of this lane
+            const int64_t orow = (MODE == kDw ? (int64_t)t.e * q.p.n : 0) + t.row0;
+            // Scales of int8 products come in while the sums are still being formed: of the
+            // columns and rows that a fragment gives this lane, or of its column and row.
+            float cs[4], rs[kBatches][kF32 ? 1 : 16];
             if (kI8) {
                 const float *ws = q.p.w_scale + (int64_t)t.e * q.p.n, *xs = q.p.x_scale + t.row0;
-                if (q.staged) {
 #pragma unroll
-                    for (int j = 0; j < 4; j++) fcs[j] = ws[min(col - lane + 8 * j + (lane >> 2), cols - 1)];
-                } else if (mine)
-                    cs = ws[col];
+                for (int j = 0; j < 4; j++) cs[j] = ws[min(kF32 ? col : col - lane + 8 * j + (lane >> 2), cols - 1)];
 #pragma unroll
-                for (int h = 0; h < kAccCols / 64; h++) {
-                    const int r = first + 64 * h;
-                    if (r >= t.nrow) break;
-                    if (q.staged) {
+                for (int h = 0; h < kBatches; h++)
 #pragma unroll
-                        for (int j = 0; j < 8; j++) frs[h][j] = xs[min(r + 8 * (j >> 1) + 2 * (lane & 3) + (j & 1), t.nrow - 1)];
-                    } else
-                        rs[h] = r + lane < t.nrow ? xs[r + lane] : 0.0f;
-                }
+                    for (int j = 0; j < (kF32 ? 1 : 16); j++)
+                        rs[h][j] = xs[min(kBatch * (2 * h + half) + (kF32 ? lane : 8 * (j >> 1) + 2 * (lane & 3) + (j & 1)), t.nrow - 1)];
             }
             const int buf = it & 1;
             if (!none) {
                 it++;
-                if (!half_all(warp >> 2, mbar_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, g_status, 5))) break;
+                if (!half_all(half, mbar_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, g_status, 5))) break;
                 acc_phase ^= 1u << buf;
                 tc_fence_after();
             }
+            // this warp has read what it needs of the accumulator
+            auto release = [&]() {
+                if (none) return;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 1)
+                        mbar_arrive(&bars->acc_empty[buf]);
+                    else
+                        mbar_arrive_cluster(mapa_shared(&bars->acc_empty[buf], 0));
+                }
+            };
+            if (kBatch * half >= t.nrow) release();
             const uint32_t tbase = tmem_base + buf * kAccCols + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll
-            for (int h = 0; h < kAccCols / 64; h++) {
-                const int r = first + 64 * h;
+            for (int h = 0; h < kBatches; h++) {
+                const int r = kBatch * (2 * h + half);
                 if (r >= t.nrow) break;
-                const int n = min(32, t.nrow - r);
-                if (q.staged) {
-                    // 16 bits: fragments of 16 lanes x 8 columns hold two rows' values of a
-                    // column to a thread, which is what a transposing matrix store takes: 32
-                    // rows x 128 columns are staged by four of them a warp and leave as whole
-                    // boxes (two of 64 columns), or, at a group's end, in 16-byte pieces. Shared
-                    // memory is what the MMAs run on (each stage's bytes pass it twice in the
-                    // time of its MMAs), so what counts here is how few passes this takes.
-                    const int half = warp >> 2;
-                    uint8_t *os = out_stage + half * kOutBytes;
-                    uint32_t f[2][16];
+                const int n = min(kBatch, t.nrow - r);
+                const bool last = r + 2 * kBatch >= t.nrow;
+                if constexpr (!kF32) {
+                    // Fragments of 16 lanes x 8 columns hold two rows' values of a column to a
+                    // thread, which is what a transposing matrix store takes.
+                    uint32_t f[2][2][16];
                     __syncwarp();
                     if (!none) {
-                        tmem_ld_frag(tbase + r, f[0]);
-                        tmem_ld_frag(tbase + (16u << 16) + r, f[1]);
+#pragma unroll
+                        for (int s = 0; s < 2; s++)
+#pragma unroll
+                            for (int b = 0; b < 2; b++) tmem_ld_frag(tbase + ((uint32_t)(16 * b) << 16) + r + 32 * s, f[s][b]);
                         tmem_ld_wait();
                     }
-                    uint32_t w[4][4];   // [8 rows][8 columns], two rows to a word
+                    if (last) release();
+                    uint32_t w[8][4];   // [8 rows][8 columns], two rows to a word
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
+                    for (int i = 0; i < 8; i++)
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
-                            const uint32_t u0 = f[j >> 1][4 * i + 2 * (j & 1)], u1 = f[j >> 1][4 * i + 2 * (j & 1) + 1];
-                            float v0 = __uint_as_float(u0), v1 = __uint_as_float(u1);
+                            const uint32_t *u = &f[i >> 2][j >> 1][4 * (i & 3) + 2 * (j & 1)];
+                            float v0 = __uint_as_float(u[0]), v1 = __uint_as_float(u[1]);
                             if (kI8) {
-                                v0 = (float)(int32_t)u0 * (frs[h][2 * i] * fcs[j]);
-                                v1 = (float)(int32_t)u1 * (frs[h][2 * i + 1] * fcs[j]);
+                                v0 = (float)(int32_t)u[0] * (rs[h][2 * i] * cs[j]);
+                                v1 = (float)(int32_t)u[1] * (rs[h][2 * i + 1] * cs[j]);
                             }
                             w[i][j] = none ? 0u : q.out_type == NVFP4_MOE_TYPE_BF16 ? pack_bf16(v0, v1) : pack_f16(v0, v1);
                         }
-                    if (quarter == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    half_sync(half);   // the previous chunk has left
+                    if (storer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    half_sync(half);   // the previous batch has left
+                    // [64 columns' half][row][128 bytes] in the 128-byte swizzle
                     const int piece = 4 * quarter + (lane >> 3), k = lane & 7;
                     uint8_t *to = os + (piece >> 3) * (kOutBytes / 2) + k * 128 + (((piece & 7) ^ k) << 4);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) stmatrix_trans(to + i * 8 * 128, w[i]);
-                    const int ocol = t.m0 + rank * 128, orow = (MODE == kDw ? t.e * q.p.n : 0) + t.row0 + r;
-                    if (n == kOutRows) {
+                    for (int i = 0; i < 8; i++) stmatrix_trans(to + i * 8 * 128, w[i]);
+                    if (q.staged && n == kBatch) {   // whole boxes
                         fence_proxy_async_smem();
                         half_sync(half);
-                        if (quarter == 0 && lane == 0)
-                            for (int b = 0; b < 2; b++)
-                                if (ocol + 64 * b < cols) tma_store_2d(&map_o, os + b * (kOutBytes / 2), ocol + 64 * b, orow);
-                    } else {
+                        if (storer) {
+                            if (col0 < cols) tma_store_2d(&map_o, os, col0, (int)(orow + r));
+                            if (col0 + 64 < cols) tma_store_2d(&map_o, os + kOutBytes / 2, col0 + 64, (int)(orow + r));
+                            bulk_commit();
+                        }
+                    } else {   // a group's end, or rows that a box cannot have: 16 bytes at a time
                         half_sync(half);
                         for (int i = 32 * quarter + lane; i < n * 16; i += 128) {
-                            const int row = i >> 4, pc = i & 15, c0 = ocol + 8 * pc;
+                            const int row = i >> 4, pc = i & 15, c0 = col0 + 8 * pc;
                             const uint4 v = *reinterpret_cast<const uint4 *>(os + (pc >> 3) * (kOutBytes / 2) + row * 128 +
                                                                              (((pc & 7) ^ (row & 7)) << 4));
-                            uint16_t *o = static_cast<uint16_t *>(q.p.out) + (int64_t)(orow + row) * q.p.out_ld + c0;
-                            if (c0 + 8 <= cols)
+                            uint16_t *o = static_cast<uint16_t *>(q.p.out) + (orow + r + row) * q.p.out_ld + c0;
+                            if (q.staged && c0 + 8 <= cols)
                                 *reinterpret_cast<uint4 *>(o) = v;
-                            else
+                            else {
+                                const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
                                 for (int c = 0; c < 8; c++)
-                                    if (c0 + c < cols) o[c] = (uint16_t)((c & 1 ? (&v.x)[c >> 1] >> 16 : (&v.x)[c >> 1]) & 0xffff);
+                                    if (c0 + c < cols) o[c] = (uint16_t)(e[c >> 1] >> (16 * (c & 1)));
+                            }
                         }
                     }
-                    continue;
-                }
-                float v[32];
-                if (none) {
-#pragma unroll
-                    for (int j = 0; j < 32; j++) v[j] = 0.0f;
                 } else {
+                    float v[32];
                     uint32_t u[32];
                     __syncwarp();
-                    tmem_ld32(tbase + r, u);
-                    tmem_ld_wait();
+                    if (!none) {
+                        tmem_ld32(tbase + r, u);
+                        tmem_ld_wait();
+                    }
+                    if (last) release();
 #pragma unroll
                     for (int j = 0; j < 32; j++)
-                        v[j] = kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs[h], j) * cs) : __uint_as_float(u[j]);
+                        v[j] = none ? 0.0f
+                               : kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs[h][0], j) * cs[0])
+                                     : __uint_as_float(u[j]);
+                    if (q.staged && n == kBatch) {
+                        if (storer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        half_sync(half);
+                        float *to = reinterpret_cast<float *>(os) + 32 * quarter + lane;   // [row][128 columns]
+#pragma unroll
+                        for (int j = 0; j < 32; j++) to[128 * j] = v[j];
+                        fence_proxy_async_smem();
+                        half_sync(half);
+                        if (storer && col0 < cols) {
+                            tma_store_2d(&map_o, os, col0, (int)(orow + r));
+                            bulk_commit();
+                        }
+                    } else if (col < cols) {   // a warp has 128 bytes of a row as it is
+                        float *o = static_cast<float *>(q.p.out) + (orow + r) * q.p.out_ld + col;
+                        if (q.p.out_add) {
+                            float b[32];
+#pragma unroll
+                            for (int j = 0; j < 32; j++) b[j] = j < n ? o[j * q.p.out_ld] : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 32; j++) v[j] += b[j];
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; j++)
+                            if (j < n) o[j * q.p.out_ld] = v[j];
+                    }
                 }
-                if (mine) {
-                    const int64_t o = at + r * q.p.out_ld;
-                    if (q.out_type == NVFP4_MOE_TYPE_F32)
-                        store_rows(static_cast<float *>(q.p.out) + o, q.p.out_ld, v, n, q.p.out_add);
-                    else if (q.out_type == NVFP4_MOE_TYPE_BF16)
-                        store_rows(static_cast<__nv_bfloat16 *>(q.p.out) + o, q.p.out_ld, v, n, false);
-                    else
-                        store_rows(static_cast<__half *>(q.p.out) + o, q.p.out_ld, v, n, false);
-                }
-            }
-            if (!none) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_leader<CG>(&bars->acc_empty[buf]);
             }
         }
-        if (quarter == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (storer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     __syncwarp();
@@ -785,23 +792,31 @@ bool map_operand(CUtensorMap *m, const Operand &o, nvfp4_moe_type type, int rows
            CUDA_SUCCESS;
 }
 
-// 16-bit output rows as a store target: boxes of 64 columns x kOutRows rows in the 128-byte swizzle.
+// Output rows as a store target: 16 bits in boxes of 64 columns x 64 rows in the 128-byte
+// swizzle, 32 bits in plain boxes of 128 columns x 32 rows.
 bool map_output(CUtensorMap *m, void *base, nvfp4_moe_type type, int64_t rows, int64_t cols, int64_t ld) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(ld * 2)};
-    const cuuint32_t box[2] = {64, kOutRows}, ones[2] = {1, 1};
-    return fn(m, map_type(type), 2, base, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const bool f32 = type == NVFP4_MOE_TYPE_F32;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(ld * (f32 ? 4 : 2))};
+    const cuuint32_t box[2] = {f32 ? 128u : 64u, f32 ? 32u : 64u}, ones[2] = {1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : map_type(type), 2, base, dims, strides, box, ones,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 typedef void (*MmaKernel)(const MmaParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap);
 
-MmaKernel kernel_of(int mode, bool i8, int cg) {
-    if (i8) return cg == 1 ? product_mma_kernel<kFwd, true, 1> : product_mma_kernel<kFwd, true, 2>;
-    if (mode == kFwd) return cg == 1 ? product_mma_kernel<kFwd, false, 1> : product_mma_kernel<kFwd, false, 2>;
-    if (mode == kDx) return cg == 1 ? product_mma_kernel<kDx, false, 1> : product_mma_kernel<kDx, false, 2>;
-    return cg == 1 ? product_mma_kernel<kDw, false, 1> : product_mma_kernel<kDw, false, 2>;
+template <int CG, bool kF32>
+MmaKernel kernel_of(int mode, bool i8) {
+    if (i8) return product_mma_kernel<kFwd, true, CG, kF32>;
+    return mode == kFwd ? product_mma_kernel<kFwd, false, CG, kF32>
+           : mode == kDx ? product_mma_kernel<kDx, false, CG, kF32>
+                         : product_mma_kernel<kDw, false, CG, kF32>;
+}
+MmaKernel kernel_of(int mode, bool i8, int cg, bool f32) {
+    return cg == 1 ? (f32 ? kernel_of<1, true>(mode, i8) : kernel_of<1, false>(mode, i8))
+                   : (f32 ? kernel_of<2, true>(mode, i8) : kernel_of<2, false>(mode, i8));
 }
 
 cudaLaunchConfig_t config(int grid, int cg, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr) {
@@ -834,17 +849,16 @@ cudaError_t resident(Resident *out) {
     std::lock_guard<std::mutex> lock(g_mu);
     Resident &r = g_resident[dev];
     if (!r.done) {
-        for (int mode = 0; mode < 4; mode++)
-            for (int cg = 1; cg <= 2; cg++) {
-                e = cudaFuncSetAttribute(kernel_of(mode % 3, mode == 3, cg), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)kSmemLimit);
-                if (e != cudaSuccess) return e;
-            }
+        for (int i = 0; i < 16; i++) {
+            e = cudaFuncSetAttribute(kernel_of(i % 4 % 3, i % 4 == 3, 1 + (i >> 2 & 1), i >> 3),
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
+            if (e != cudaSuccess) return e;
+        }
         e = cudaDeviceGetAttribute(&r.ctas, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute attr;
         const cudaLaunchConfig_t cfg = config(2, 2, kSmemLimit, 0, &attr);
-        e = cudaOccupancyMaxActiveClusters(&r.pairs, kernel_of(kFwd, false, 2), &cfg);
+        e = cudaOccupancyMaxActiveClusters(&r.pairs, kernel_of(kFwd, false, 2, false), &cfg);
         if (e != cudaSuccess) return e;
         if (r.pairs < 1) return cudaErrorInvalidConfiguration;
         r.done = true;
@@ -884,7 +898,7 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     q.a_whole = mode != kFwd && oa.cols % 64 == 0;
     q.b_whole = mode == kDw && ob.cols % 64 == 0 && p.n % (64 * cg) == 0;
     const int64_t out_rows = mode == kDw ? (int64_t)p.groups * p.n : p.rows;
-    q.staged = out != NVFP4_MOE_TYPE_F32 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.out_ld % 8 == 0;
+    q.staged = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.out_ld % (out == NVFP4_MOE_TYPE_F32 ? 4 : 8) == 0 && !p.out_add;
     CUtensorMap a, b, b_small, o;
     bool ok = map_operand(&a, oa, type, mode == kFwd ? 128 : 64, q.a_whole ? 2 : 0) &&
               map_operand(&b, ob, type, mode == kDw ? 64 : q.box, q.b_whole ? q.bn / cg / 64 : 0);
@@ -899,7 +913,7 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     const int units = (int)std::min<int64_t>(cg == 2 ? r.pairs : r.ctas, std::max<int64_t>(most, 1));
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = config(units * cg, cg, smem_bytes(q.bn, cg, q.stages), s, &attr);
-    return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg), q, a, b, b_small, o);
+    return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg, out == NVFP4_MOE_TYPE_F32), q, a, b, b_small, o);
 }
 
 int product_status(cudaStream_t s) {
