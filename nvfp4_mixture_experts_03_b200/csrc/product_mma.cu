@@ -256,9 +256,18 @@ __device__ inline bool mbar_test(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
+__device__ inline bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r != 0;
+}
+// A value that every lane has, as the compiler can see it.
+__device__ inline int uni(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // A bounded wait by a whole warp, with one answer for all its lanes.
 template <bool kCluster>
 __device__ inline bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where) {
+    if (__all_sync(0xffffffffu, mbar_try_wait<kCluster>(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, abort, g_status, where));
 }
 
@@ -319,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Groups *groups = reinterpret_cast<Groups *>(bars + 1);
     volatile int *abort = &bars->abort;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
     const int cid = (int)blockIdx.x / CG, ncl = (int)gridDim.x / CG;
     const int S = q.stages;
@@ -419,59 +428,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == S) { stage = 0; phase ^= 1; }
     };
 
+    // The TMA and the MMA warp run their loops converged, with warp-uniform values (uni), and
+    // one elected lane issues: the copies and MMAs take their descriptors and coordinates
+    // from uniform registers, which a loop inside `if (lane == 0)` has to fill one by one
+    // before each of them.
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA
         uint32_t issued = 0, issued_phase = 0;   // stages loaded, and the parity of their last use
         bool ok = true;
+        const bool elected = elect_one();
         while (ok) {
             const OutTile t = next_tile();
-            if (t.e < 0) break;
-            if (lane == 0) {
-                const int half = cdiv(t.nrow, 16 * CG) * 16;   // B columns of this CTA
-                const int brow = t.row0 + rank * half, acol = t.m0 + rank * 128;
-                // A copy costs the TMA unit much the same whatever its rows: few and large ones
-                // (one box of 128 rows instead of four of 32: 435 -> 373 us for 8192 x 8192 x
-                // 4096), small ones where the tile has few rows.
-                const bool few = half <= 2 * kBoxSmall;
-                const int box = MODE == kDw ? 64 : few ? kBoxSmall : q.box;
-                const int nbox = MODE == kDw ? q.b_whole ? q.bn / CG / 64 : cdiv(half, 64) : cdiv(half, box);
-                const CUtensorMap *mb = MODE != kDw && few ? &map_b_small : &map_b;
-                const uint32_t bytes = kABytes + nbox * box * kLine;
-                for (int c = 0; c < t.c; c += kStep) {
-                    if (!mbar_wait<CG == 2>(&bars->empty[stage], phase ^ 1, abort, g_status, 1)) { ok = false; break; }
-                    uint8_t *a = smem + stage * stage_size, *b = a + kABytes;
-                    // A stage whose last rows have to be zeroed is counted by each CTA for
-                    // itself first; every other one by the leader, for both.
-                    const bool tail = MODE == kDw && t.c - c < kStep && ((t.c - c) & 15);
-                    uint64_t *bar = tail ? &bars->tail[stage] : &bars->full[stage];
-                    const uint32_t leader = CG == 1 ? 0 : mapa_shared(bar, tail ? rank : 0);
+            const int e = uni(t.e), tc = uni(t.c), c0 = uni(t.c0), half = uni(cdiv(t.nrow, 16 * CG) * 16);   // B columns of this CTA
+            if (e < 0) break;
+            const int brow = uni(t.row0) + rank * half, acol = uni(t.m0) + rank * 128;
+            // A copy costs the TMA unit much the same whatever its rows: few and large ones
+            // (one box of 128 rows instead of four of 32: 435 -> 373 us for 8192 x 8192 x
+            // 4096), small ones where the tile has few rows.
+            const bool few = half <= 2 * kBoxSmall;
+            const int box = MODE == kDw ? 64 : few ? kBoxSmall : q.box;
+            const int nbox = MODE == kDw ? q.b_whole ? q.bn / CG / 64 : cdiv(half, 64) : few ? cdiv(half, kBoxSmall) : half > q.box ? 2 : 1;
+            const CUtensorMap *mb = MODE != kDw && few ? &map_b_small : &map_b;
+            const uint32_t bytes = kABytes + nbox * box * kLine;
+            const int z = MODE == kDw ? 0 : e;
+            for (int c = 0; c < tc; c += kStep) {
+                if (!warp_wait<CG == 2>(&bars->empty[stage], phase ^ 1, abort, 1)) { ok = false; break; }
+                uint8_t *a = smem + stage * stage_size, *b = a + kABytes;
+                // A stage whose last rows have to be zeroed is counted by each CTA for
+                // itself first; every other one by the leader, for both.
+                const bool tail = MODE == kDw && tc - c < kStep && ((tc - c) & 15);
+                uint64_t *bar = tail ? &bars->tail[stage] : &bars->full[stage];
+                const uint32_t leader = CG == 1 ? 0 : mapa_shared(bar, tail ? rank : 0);
+                issued |= 1u << stage;
+                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                if (elected) {
                     if (tail)
                         mbar_arrive_expect_tx(bar, bytes);
                     else if (rank == 0)
                         mbar_arrive_expect_tx(bar, CG * bytes);
-                    issued |= 1u << stage;
-                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-                    const int z = MODE == kDw ? 0 : t.e;
                     if (MODE == kFwd)
                         tma_3d<CG>(a, &map_a, bar, leader, c, acol, z);
                     else if (q.a_whole)
-                        tma_4d<CG>(a, &map_a, bar, leader, acol / 64, t.c0 + c, z);
+                        tma_4d<CG>(a, &map_a, bar, leader, acol / 64, c0 + c, z);
                     else
                         for (int h = 0; h < 2; h++)
-                            tma_3d<CG>(a + h * 64 * kLine, &map_a, bar, leader, acol + 64 * h, t.c0 + c, z);
+                            tma_3d<CG>(a + h * 64 * kLine, &map_a, bar, leader, acol + 64 * h, c0 + c, z);
                     if (MODE == kDw && q.b_whole)
-                        tma_4d<CG>(b, &map_b, bar, leader, brow / 64, t.c0 + c, 0);
-                    else
-                        for (int j = 0; j < nbox; j++) {
-                            if (MODE == kDw)
-                                tma_3d<CG>(b + j * 64 * kLine, mb, bar, leader, brow + 64 * j, t.c0 + c, 0);
-                            else
-                                tma_3d<CG>(b + j * box * kLine, mb, bar, leader, c, brow + j * box, 0);
-                        }
-                    next();
+                        tma_4d<CG>(b, &map_b, bar, leader, brow / 64, c0 + c, 0);
+                    else if (MODE == kDw)
+                        for (int j = 0; j < nbox; j++) tma_3d<CG>(b + j * 64 * kLine, mb, bar, leader, brow + 64 * j, c0 + c, 0);
+                    else {
+                        tma_3d<CG>(b, mb, bar, leader, c, brow, 0);
+                        if (nbox > 1) tma_3d<CG>(b + box * kLine, mb, bar, leader, c, brow + box, 0);
+                    }
                 }
+                __syncwarp();
+                next();
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
         }
         // The last load of every stage has landed before the CTA ends (after a give-up
         // nobody else has waited for them).
@@ -484,41 +497,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             uint32_t acc_phase = 0, it = 0;
             bool ok = true, ready = false;   // ready: the current stage has already been seen full
+            const bool elected = elect_one();
+            const uint32_t d0 = uni(tmem_base);
+            const uint64_t a0 = MODE == kFwd ? smem_desc_sw128(smem_u32(smem)) : desc_mn(smem_u32(smem));
+            const uint64_t b0 = MODE == kDw ? desc_mn(smem_u32(smem + kABytes)) : smem_desc_sw128(smem_u32(smem + kABytes));
             while (ok) {
                 const OutTile t = next_tile();
-                if (t.e < 0) break;
-                if (MODE == kDw && t.c == 0) continue;
+                const int e = uni(t.e), tc = uni(t.c);
+                const uint32_t idesc = q.idesc | (uint32_t)(uni(cdiv(t.nrow, 16 * CG)) * 2 * CG) << 17;
+                if (e < 0) break;
+                if (MODE == kDw && tc == 0) continue;
                 const int buf = it++ & 1;
-                if (lane == 0) {
-                    const uint32_t idesc = q.idesc | (uint32_t)(cdiv(t.nrow, 16 * CG) * 2 * CG) << 17;
-                    const uint32_t d = tmem_base + buf * kAccCols;
-                    ok = mbar_wait<CG == 2>(&bars->acc_empty[buf], ((acc_phase >> buf) & 1) ^ 1, abort, g_status, 2);
+                const uint32_t d = d0 + buf * kAccCols;
+                ok = warp_wait<CG == 2>(&bars->acc_empty[buf], ((acc_phase >> buf) & 1) ^ 1, abort, 2);
+                acc_phase ^= 1u << buf;
+                tc_fence_after();
+                for (int c = 0; ok && c < tc; c += kStep) {
+                    if (!ready && !warp_wait<CG == 2>(&bars->full[stage], phase, abort, 3)) { ok = false; break; }
                     tc_fence_after();
-                    for (int c = 0; ok && c < t.c; c += kStep) {
-                        if (!ready && !mbar_wait<CG == 2>(&bars->full[stage], phase, abort, g_status, 3)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint32_t a = smem_u32(smem + stage * stage_size), b = a + kABytes;
-                        uint64_t *empty = &bars->empty[stage];
-                        // the next stage is looked at while this one's MMAs go out
-                        next();
-                        ready = mbar_test<CG == 2>(&bars->full[stage], phase);
-                        const uint64_t ad = MODE == kFwd ? smem_desc_sw128(a) : desc_mn(a);
-                        const uint64_t bd = MODE == kDw ? desc_mn(b) : smem_desc_sw128(b);
-                        // 32 bytes of K a step, or 16 rows of 128 bytes
-                        constexpr int kA = MODE == kFwd ? 2 : 16 * kLine >> 4, kB = MODE == kDw ? 16 * kLine >> 4 : 2;
-                        const int steps = MODE == kDw ? min(4, cdiv(t.c - c, 16)) : 4;
+                    // the address fields of both descriptors, in units of 16 bytes
+                    const uint64_t ad = a0 + (uint32_t)stage * (stage_size >> 4), bd = b0 + (uint32_t)stage * (stage_size >> 4);
+                    uint64_t *empty = &bars->empty[stage];
+                    // the next stage is looked at while this one's MMAs go out
+                    next();
+                    // 32 bytes of K a step, or 16 rows of 128 bytes
+                    constexpr int kA = MODE == kFwd ? 2 : 16 * kLine >> 4, kB = MODE == kDw ? 16 * kLine >> 4 : 2;
+                    const int steps = MODE == kDw ? min(4, cdiv(tc - c, 16)) : 4;
+                    if (elected) {
 #pragma unroll
                         for (int s = 0; s < 4; s++)
-                            if (s < steps) mma<CG, kI8>(d, ad + s * kA, bd + s * kB, idesc, (c | s) != 0);
+                            if (s < steps) mma<CG, kI8>(d, ad + s * kA, bd + s * kB, idesc, s ? 1u : (uint32_t)c);
                         commit<CG>(empty);
                     }
-                    if (ok) commit<CG>(&bars->acc_full[buf]);
+                    __syncwarp();
+                    ready = __all_sync(0xffffffffu, mbar_test<CG == 2>(&bars->full[stage], phase));
                 }
-                acc_phase ^= 1u << buf;
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (ok && elected) commit<CG>(&bars->acc_full[buf]);
+                __syncwarp();
             }
-            // every MMA this thread issued completes before TMEM is freed
-            if (lane == 0) {
+            // every MMA that was issued completes before TMEM is freed
+            if (elected) {
                 if (CG == 1)
                     commit<1>(&bars->drain);
                 else
