@@ -62,10 +62,9 @@ constexpr int kBoxSmall = 32;           // rows of the smaller K-major B box
 constexpr int kOutBytes = 16 * 1024;    // a half's staged outputs: 64 rows x 128 columns of 16 bits, 32 of 32
 
 struct __align__(16) Bars {
-    uint64_t full[kMaxStages];    // leader: its one arrival, and the bytes of every CTA of the group
+    uint64_t full[kMaxStages];    // leader: an arrival for each CTA of the group, and all their bytes
     uint64_t empty[kMaxStages];   // each CTA: the MMAs' commit
     uint64_t tail[kMaxStages];    // dw, each CTA: its own bytes of a stage with rows to zero
-    uint64_t peer[kMaxStages];    // dw, leader: the other CTA has zeroed its rows of a stage
     uint64_t acc_full[2];         // each CTA: the MMAs' commit
     uint64_t acc_empty[2];        // leader: the epilogue warps of each CTA
     uint64_t tile_full[kTilesAhead];    // the tile warp's entry
@@ -88,7 +87,7 @@ struct __align__(16) OutTile {
 struct Groups {
     OutTile ahead[kTilesAhead];
     int32_t lo[NVFP4_MOE_MAX_GROUPS + 1];   // first row, and the last group's end
-    int32_t before[NVFP4_MOE_MAX_GROUPS + 1];
+    int32_t before[NVFP4_MOE_MAX_GROUPS + 1];   // (dw: the groups by falling rows)
     int32_t warp_sum[kThreads / 32], warp_max[kThreads / 32];
 };
 
@@ -292,8 +291,9 @@ struct Tiles {
         t.m0 = j / high * 128 * CG;
         if (MODE == kDw) {
             const int nt = cdiv(q.p.n, q.bn);
-            t.e = r / nt;
-            t.row0 = (r - t.e * nt) * q.bn;
+            const int at = r / nt;
+            t.e = g.before[at] & 1023;
+            t.row0 = (r - at * nt) * q.bn;
             t.nrow = min(q.bn, q.p.n - t.row0);
             t.c0 = g.lo[t.e];
             t.c = g.lo[t.e + 1] - t.c0;
@@ -336,10 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; s++) {
-            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->full[s], CG);
             mbar_init(&bars->empty[s], 1);
             mbar_init(&bars->tail[s], 1);
-            mbar_init(&bars->peer[s], 1);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(&bars->acc_full[b], 1);
@@ -397,8 +396,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 0; w < warp; w++) upto += groups->warp_sum[w];
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
-            if (e0 + i <= E) groups->before[e0 + i] = upto;
+            if (MODE != kDw && e0 + i <= E) groups->before[e0 + i] = upto;
             upto += tiles[i];
+        }
+        if (MODE == kDw) {
+            // The groups by falling rows (a bitonic sort of count | group), so that the tiles,
+            // dealt out back and forth, come to about the same work for every CTA: 64 experts
+            // of uneven popularity took 139 us in their own order and 109 us evenly filled.
+            int all = 1;
+            while (all < E) all *= 2;
+            uint32_t *key = reinterpret_cast<uint32_t *>(groups->before);
+            for (int e = threadIdx.x; e < all; e += kThreads)
+                key[e] = e < E ? (uint32_t)min(groups->lo[e + 1] - groups->lo[e], (1 << 21) - 1) << 10 | e : 0u;
+            for (int size = 2; size <= all; size *= 2)
+                for (int d = size / 2; d > 0; d /= 2) {
+                    __syncthreads();
+                    for (int x = threadIdx.x; x < all / 2; x += kThreads) {
+                        const int i = 2 * x - (x & (d - 1)), j = i + d;
+                        const uint32_t u = key[i], v = key[j];
+                        if ((u < v) == ((i & size) == 0)) {
+                            key[i] = v;
+                            key[j] = u;
+                        }
+                    }
+                }
         }
     }
     tc_fence_before();
@@ -464,8 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elected) {
                     if (tail)
                         mbar_arrive_expect_tx(bar, bytes);
-                    else if (rank == 0)
+                    else if (rank == 0) {
                         mbar_arrive_expect_tx(bar, CG * bytes);
+                        if (CG == 2) mbar_arrive(bar);   // the other CTA's arrival, which would take its time
+                    }
                     if (MODE == kFwd)
                         tma_3d<CG>(a, &map_a, bar, leader, c, acol, z);
                     else if (q.a_whole)
@@ -562,16 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tail_phase ^= 1u << last;
                     uint8_t *a = smem + last * stage_size, *b = a + kABytes;
                     const int pad = 16 - (left & 15), nb = cdiv(half, 64);   // rows to zero, in each 64-column box
-                    for (int l = lane; l < pad * (2 + nb) * 8; l += 32) {
-                        const int piece = l & 7, line = l >> 3, box = line / pad, r = left + line - box * pad;
-                        uint8_t *base = box < 2 ? a + box * 64 * kLine : b + (box - 2) * 64 * kLine;
-                        *reinterpret_cast<uint4 *>(base + r * kLine + piece * 16) = make_uint4(0, 0, 0, 0);
+                    for (int box = lane >> 3; box < 2 + nb; box += 4) {
+                        uint8_t *to = (box < 2 ? a + box * 64 * kLine : b + (box - 2) * 64 * kLine) + left * kLine + (lane & 7) * 16;
+#pragma unroll 4
+                        for (int r = 0; r < pad; r++) *reinterpret_cast<uint4 *>(to + r * kLine) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    // the leader's own rows and its peer's: one arrival for both
-                    if (CG == 2 && rank == 0 && !warp_wait<true>(&bars->peer[last], parity, abort, 6)) break;
-                    if (lane == 0) arrive_leader<CG>(rank == 0 ? &bars->full[last] : &bars->peer[last]);
+                    if (lane == 0) arrive_leader<CG>(&bars->full[last]);
                 }
                 stage = (stage + steps) % S;
             }
@@ -579,9 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kTileWarp) {
         // ---------------------------------------------------- lists the tiles
         const Tiles<MODE, CG> tiles(q, *groups);
-        for (int i = cid; ; i += ncl) {
+        for (int round = 0; ; round++) {
             OutTile t;
             t.e = -1;
+            const int i = round * ncl + (MODE == kDw && (round & 1) ? ncl - 1 - cid : cid);
             if (i < tiles.total) t = tiles.at(i);
             if (!warp_wait<false>(&bars->tile_empty[slot], slot_phase ^ 1, abort, 8)) break;
             if (lane == 0) {
