@@ -907,6 +907,39 @@ cudaError_t resident(Resident *out) {
     return cudaSuccess;
 }
 
+// The tile shape: CTAs to a tile and its most rows.
+struct Shape {
+    int cg, bn;
+};
+
+// By an estimate of the time, in cycles of a CTA (or pair), for groups of average size:
+// waves of tiles, each as long as the longer of its sum and its epilogue. A stage of a tile
+// with N columns takes about max(380, 3.7 N) cycles in one CTA and max(400, 2.75 N) in a pair
+// (all SMs busy, operands in L2), 32 columns of an epilogue 420 (16 bits); a tile costs 1200
+// besides, a pair 2000 once. Small tiles fill the GPU where there are few rows (201 rows x
+// 2048 x 768 int8: 6.4 us in tiles of 64, 9.7 in pairs of 256), pairs of 256 move the fewest
+// bytes an MMA (4096 x 2560 x 2560 BF16: 44 us, 69 in tiles of 64; 64 experts, 16384 pairs,
+// dx: 121 us, 131 in tiles of 64).
+Shape choose(int mode, const Product &p, bool i8, int cols, const Resident &r) {
+    static const Shape shapes[] = {{1, 64}, {1, 128}, {2, 128}, {2, 256}};
+    const int active = std::min(p.groups, p.rows), avg = cdiv(p.rows, active), step = i8 ? 128 : 64;
+    Shape best = shapes[0];
+    int64_t least = INT64_MAX;
+    for (const Shape &s : shapes) {
+        const int total = mode == kDw ? p.n : avg, nt = cdiv(total, s.bn), n = cdiv(total, nt);
+        const int64_t tiles = (int64_t)cdiv(cols, 128 * s.cg) * nt * active;
+        const int stages = cdiv(mode == kFwd ? p.k : mode == kDx ? p.n : avg, step);
+        const int64_t sum = (int64_t)stages * (s.cg == 1 ? std::max(380, n * 37 / 10) : std::max(400, n * 11 / 4));
+        const int64_t units = s.cg == 1 ? r.ctas : r.pairs;
+        const int64_t cost = (tiles + units - 1) / units * (std::max<int64_t>(sum, n * 13) + 1200) + (s.cg == 2 ? 2000 : 0);
+        if (cost <= least) {   // of equals the larger: groups are seldom all of a size
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, nvfp4_moe_type out, cudaStream_t s) {
@@ -923,9 +956,9 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     MmaParams q{};
     q.p = p;
     q.out_type = out;
-    const int avg = mode == kDw ? p.n : cdiv(p.rows, p.groups);
-    const int cg = avg >= 256 && cols > 128 ? 2 : 1;
-    q.bn = cg == 2 ? 256 : avg >= 128 ? 256 : avg > 32 || mode == kDw ? 128 : 64;
+    const Shape shape = choose(mode, p, i8, cols, r);
+    const int cg = shape.cg;
+    q.bn = shape.bn;
     q.box = std::min(128, q.bn / cg);
     q.stages = (int)std::min<size_t>(kMaxStages, (kSmemLimit - smem_bytes(q.bn, cg, 0)) / stage_bytes(q.bn, cg));
     // D F32 (or S32), A and B F16, BF16 or S8, their majors, M
@@ -940,9 +973,10 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     const int64_t out_rows = mode == kDw ? (int64_t)p.groups * p.n : p.rows;
     q.staged = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.out_ld % (out == NVFP4_MOE_TYPE_F32 ? 4 : 8) == 0 && !p.out_add;
     CUtensorMap a, b, b_small, o;
-    bool ok = map_operand(&a, oa, type, mode == kFwd ? 128 : 64, q.a_whole ? 2 : 0) &&
-              map_operand(&b, ob, type, mode == kDw ? 64 : q.box, q.b_whole ? q.bn / cg / 64 : 0);
-    b_small = o = b;   // where they are not used
+    bool ok = map_operand(&a, oa, type, mode == kFwd ? 128 : 64, q.a_whole ? 2 : 0);
+    b = b_small = o = a;   // where they are not used
+    if (ok && (mode == kDw || q.bn / cg > 2 * kBoxSmall))
+        ok = map_operand(&b, ob, type, mode == kDw ? 64 : q.box, q.b_whole ? q.bn / cg / 64 : 0);
     if (ok && mode != kDw) ok = map_operand(&b_small, ob, type, kBoxSmall, 0);
     if (ok && q.staged) ok = map_output(&o, p.out, out, out_rows, cols, p.out_ld);
     if (!ok) return cudaErrorInvalidValue;

@@ -175,7 +175,20 @@ cudaError_t launch(const Product &p, nvfp4_moe_type out, cudaStream_t s) {
 
 }  // namespace
 
-bool product_streams(int mode, const Product &p) { return mode == kFwd && p.rows <= 32; }
+// Streaming reads a group's matrix again for every batch of its rows, and has a CTA for every
+// 16 columns of each; the tensor-core tiles have some 6 us of start and end. Measured against
+// them (us, streamed / tiles): dense 8 x 8192 x 8192 BF16 26 / 31, 16 x the same 42 / 32, 64 x
+// 1536 x 2048 8.6 / 10.2, 64 x 2560 x 2560 14.6 / 11.5, 512 x 256 x 256 4.2 / 6.1, 32 x 8192 x 256
+// 6.8 / 6.1; by group 32 rows of 8 x 256 x 256 3.3 / 6.5, 64 of 16 x 512 x 512 7.4 / 7.1, 10 of 64 x
+// 1536 x 2048 11.5 / 12.1, 32 of the same 32.6 / 28.6.
+bool product_streams(int mode, const Product &p, int elem_bytes) {
+    if (mode != kFwd) return false;
+    const int64_t blocks = cdiv(p.n, kCols);
+    if (p.offsets) return p.rows * blocks <= 1536;
+    if (p.rows <= 8) return true;
+    const int64_t passes = cdiv(p.rows, 32);
+    return passes * blocks <= 296 && passes * p.n * p.k * elem_bytes <= 14000000;
+}
 
 cudaError_t launch_product_stream(const Product &p, nvfp4_moe_type type, nvfp4_moe_type out, cudaStream_t s) {
     return type == NVFP4_MOE_TYPE_INT8   ? launch<int8_t>(p, out, s)

@@ -75,7 +75,7 @@ int product(int mode, const nvfp4_moe_gemm_io *io, void *stream) {
     p.w_scale = io->w_scale;
     p.out = io->out;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = product_streams(mode, p) ? launch_product_stream(p, io->type, io->out_type, s)
+    const cudaError_t e = product_streams(mode, p, es) ? launch_product_stream(p, io->type, io->out_type, s)
                                                    : launch_product_mma(mode, p, io->type, io->out_type, s);
     return e == cudaSuccess ? NVFP4_MOE_OK : NVFP4_MOE_ERR_CUDA;
 }

@@ -44,7 +44,7 @@ __device__ inline float from_f32(float v) { return v; }
 cudaError_t launch_quantize(const nvfp4_moe_quantize_io &io, cudaStream_t s);
 cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, nvfp4_moe_type out_type,
                                cudaStream_t s);
-bool product_streams(int mode, const Product &p);   // few enough rows to be streamed
+bool product_streams(int mode, const Product &p, int elem_bytes);   // few enough rows to be streamed
 cudaError_t launch_product_stream(const Product &p, nvfp4_moe_type type, nvfp4_moe_type out_type, cudaStream_t s);
 int product_status(cudaStream_t s);   // the first wait that gave up on the current device, cleared
 
