@@ -16,6 +16,7 @@ are allocated on it.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 import torch
 
@@ -61,85 +62,126 @@ def nvfp4_moe_products_status(stream: int) -> int:
     return lib().nvfp4_moe_products_status(C.c_void_p(stream))
 
 
-# ---------------------------------------------------------------- torch glue
-
 def products_status(stream=None) -> int:
     """Synchronises and returns the first device-side error of the products on the current
     device since the last read (0 if none), clearing it."""
     return nvfp4_moe_products_status((stream if stream is not None else torch.cuda.current_stream()).cuda_stream)
 
 
-# These run before every launch, so what a good call needs is kept short: messages are put
-# together only where a check fails.
+# ---------------------------------------------------------------- torch glue
+#
+# These run before every launch, and a decode product takes the GPU two or three
+# microseconds: what a good call needs is written out and kept short, the structures are
+# packed rather than built field by field, and messages are put together only where a check
+# fails.
 
 _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stream().cuda_stream, without its object
+_empty = torch.empty
 _UNIT = {torch.bfloat16: 8, torch.float16: 8, torch.float32: 4, torch.int8: 16}   # values in 16 bytes
+_pack_gemm = struct.Struct("@7iPPqPPqPqPPq").pack     # GemmIO
+_pack_quantize = struct.Struct("@4iPqPqP").pack       # QuantizeIO
 
 
-def _device_of(t, what: str) -> int:
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{what}: expected CUDA tensors")
-    return index
+def _refuse(what: str):
+    raise ValueError(what)
 
 
 def _vector(t, n: int, dtype, name: str, index: int) -> int:
     """The address of n contiguous values."""
-    if t.dtype != dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
-        raise ValueError(f"{name}: expected {n} contiguous {dtype} values on cuda:{index}")
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+        _refuse(f"{name}: expected {n} contiguous {dtype} values on cuda:{index}")
     return t.data_ptr()
 
 
 def _row_stride(t, rows: int, cols: int, name: str, index: int) -> int:
     """The row stride of [rows][cols] with contiguous rows."""
-    if t.dim() != 2 or t.get_device() != index:
-        raise ValueError(f"{name}: expected a matrix on cuda:{index}")
+    if t.get_device() != index:
+        _refuse(f"{name}: expected a tensor on cuda:{index}")
     ld, step = t.stride()
     if step != 1 and cols != 1:
-        raise ValueError(f"{name}: expected contiguous rows")
-    return ld if rows > 1 else _pad(cols, t.dtype)   # one row: no stride to take
+        _refuse(f"{name}: expected contiguous rows")
+    if rows > 1:
+        return ld
+    unit = _UNIT[t.dtype]
+    return -(-cols // unit) * unit   # one row: no stride to take
 
 
 def _matrix_stride(t, groups: int, n: int, k: int, name: str, index: int) -> int:
     """The row stride of [groups][n][k] or [n][k] whose matrices follow one another."""
     if t.get_device() != index:
-        raise ValueError(f"{name}: expected a tensor on cuda:{index}")
+        _refuse(f"{name}: expected a tensor on cuda:{index}")
     stride = t.stride()
     if stride[-1] != 1 and k != 1:
-        raise ValueError(f"{name}: expected contiguous rows")
+        _refuse(f"{name}: expected contiguous rows")
     if n > 1:
         ld = stride[-2]
+    elif groups > 1:
+        ld = stride[0]
     else:
-        ld = stride[0] if groups > 1 else _pad(k, t.dtype)
+        unit = _UNIT[t.dtype]
+        ld = -(-k // unit) * unit
     if groups > 1 and stride[0] != n * ld:
-        raise ValueError(f"{name}: matrices have to follow one another, n rows apart")
+        _refuse(f"{name}: matrices have to follow one another, n rows apart")
     return ld
 
 
-def _pad(cols: int, dtype) -> int:
-    unit = _UNIT[dtype]
-    return -(-cols // unit) * unit
+def _matrices(w, name: str):
+    """(groups, n, k) of [groups][n][k] or [n][k]."""
+    shape = w.shape
+    if len(shape) == 3:
+        return shape
+    if len(shape) != 2:
+        _refuse(f"{name}: expected [groups][n][k] or [n][k]")
+    return 1, shape[0], shape[1]
+
+
+def _offsets(offsets, groups: int, index: int) -> int:
+    if offsets is None:
+        if groups != 1:
+            _refuse("offsets: needed for more than one group")
+        return 0
+    return _vector(offsets, groups + 1, torch.int32, "offsets", index)
+
+
+def _output(out, shape, dtype, accumulate: bool, index: int, stream):
+    """(output, its type, its row stride): `out` checked, or a new tensor whose rows start every
+    whole number of 16 bytes, allocated on `stream`."""
+    if out is None:
+        if accumulate:
+            _refuse("accumulate: needs out")
+        t = _TYPES.get(dtype, TYPE_INT8)
+        if t == TYPE_INT8:
+            _refuse("out_dtype: expected bf16, f16 or f32")
+        out, ld = _new(shape, dtype, index, stream)
+        return out, t, ld
+    t = _TYPES.get(out.dtype, TYPE_INT8)
+    if t == TYPE_INT8 or tuple(out.shape) != tuple(shape) or (dtype is not None and out.dtype != dtype):
+        _refuse(f"out: expected {list(shape)} of {dtype or 'bf16, f16 or f32'}")
+    if len(shape) == 3:
+        return out, t, _matrix_stride(out, *shape, "out", index)
+    return out, t, _row_stride(out, *shape, "out", index)
 
 
 def _new(shape, dtype, index: int, stream):
-    """An empty tensor whose rows start every whole number of 16 bytes, allocated on `stream`."""
+    """(empty tensor whose rows start every whole number of 16 bytes, row stride)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return _new(shape, dtype, index, None)
-    cols = shape[-1]
-    ld = _pad(cols, dtype)
-    t = torch.empty((*shape[:-1], ld), dtype=dtype, device=index)
-    return t if ld == cols else t[..., :cols]
+    cols, unit = shape[-1], _UNIT[dtype]
+    if cols % unit == 0:
+        return _empty(shape, dtype=dtype, device=index), cols
+    ld = -(-cols // unit) * unit
+    return _empty((*shape[:-1], ld), dtype=dtype, device=index)[..., :cols], ld
 
 
-def _enqueue(fn, io, index: int, stream, what: str) -> None:
+def _enqueue(fn, io: bytes, index: int, stream, what: str) -> None:
     s = _raw_stream(index) if stream is None else stream.cuda_stream
     if _current_device() == index:
-        rc = fn(C.byref(io), s)
+        rc = fn(io, s)
     else:
         with torch.cuda.device(index):
-            rc = fn(C.byref(io), s)
+            rc = fn(io, s)
     if rc != OK:
         raise NVFP4MoEError(rc, what)
 
@@ -149,58 +191,38 @@ def quantize_int8(x, *, swiglu: bool = False, q=None, scale=None, stream=None):
     nearest whole number (ties to even). x: [rows][cols] bf16, f16 or f32; with `swiglu`
     [rows][2*cols] holding gate | up, and v = SiLU(gate) * up.
     Returns (q int8 [rows][cols], scale f32 [rows])."""
-    t = _TYPES.get(x.dtype, TYPE_INT8)
-    if x.dim() != 2 or t == TYPE_INT8:
-        raise ValueError("x: expected [rows][cols] bf16, f16 or f32")
-    rows, width = x.shape
-    if width == 0 or (swiglu and width % 2):
-        raise ValueError("x: expected at least one value a row (gate | up: an even number)")
-    cols = width // 2 if swiglu else width
-    index = _device_of(x, "quantize_int8")
-    x_ld = _row_stride(x, rows, width, "x", index)
+    t, shape = _TYPES.get(x.dtype, TYPE_INT8), x.shape
+    if len(shape) != 2 or t == TYPE_INT8:
+        _refuse("x: expected [rows][cols] bf16, f16 or f32")
+    rows, cols = shape
+    index = x.get_device()
+    if index < 0:
+        _refuse("quantize_int8: expected CUDA tensors")
+    x_ld = _row_stride(x, rows, cols, "x", index)
+    if swiglu:
+        if cols % 2:
+            _refuse("x: gate | up are an even number of values")
+        cols //= 2
+    if cols == 0:
+        _refuse("x: expected at least one value a row")
     if q is None:
-        q = _new((rows, cols), torch.int8, index, stream)
+        q, q_ld = _new((rows, cols), torch.int8, index, stream)
     elif q.dtype != torch.int8 or tuple(q.shape) != (rows, cols):
-        raise ValueError(f"q: expected int8 [{rows}][{cols}]")
-    q_ld = _row_stride(q, rows, cols, "q", index)
-    if scale is None:
+        _refuse(f"q: expected int8 [{rows}][{cols}]")
+    else:
+        q_ld = _row_stride(q, rows, cols, "q", index)
+    if scale is not None:
+        s_ptr = _vector(scale, rows, torch.float32, "scale", index)
+    else:
         if stream is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=index)
+            scale = _empty(rows, dtype=torch.float32, device=index)
         else:
             with torch.cuda.stream(stream):
-                scale = torch.empty(rows, dtype=torch.float32, device=index)
+                scale = _empty(rows, dtype=torch.float32, device=index)
         s_ptr = scale.data_ptr()
-    else:
-        s_ptr = _vector(scale, rows, torch.float32, "scale", index)
-    io = QuantizeIO(rows, cols, t, 1 if swiglu else 0, x.data_ptr(), x_ld, q.data_ptr(), q_ld, s_ptr)
+    io = _pack_quantize(rows, cols, t, 1 if swiglu else 0, x.data_ptr(), x_ld, q.data_ptr(), q_ld, s_ptr)
     _enqueue(lib().nvfp4_moe_quantize_int8, io, index, stream, "nvfp4_moe_quantize_int8")
     return q, scale
-
-
-def _out_type(out, shape, out_dtype) -> int:
-    """The output's type, checked against what the caller asked for."""
-    t = _TYPES.get(out_dtype if out is None else out.dtype, TYPE_INT8)
-    if t == TYPE_INT8:
-        raise ValueError("out, out_dtype: expected bf16, f16 or f32")
-    if out is not None and (tuple(out.shape) != shape or (out_dtype is not None and out.dtype != out_dtype)):
-        raise ValueError(f"out: expected {list(shape)}" + (f" of {out_dtype}" if out_dtype is not None else ""))
-    return t
-
-
-def _offsets(offsets, groups: int, index: int):
-    if offsets is None:
-        if groups != 1:
-            raise ValueError("offsets: needed for more than one group")
-        return None
-    return _vector(offsets, groups + 1, torch.int32, "offsets", index)
-
-
-def _operands(x, w, names: str):
-    """(groups, rows, n, k) of rows x and matrices w."""
-    if x.dim() != 2 or w.dim() not in (2, 3) or x.dtype != w.dtype:
-        raise ValueError(f"{names}: expected a matrix of rows, [groups][n][k] or [n][k], and one type")
-    n, k = w.shape[-2:]
-    return (w.shape[0] if w.dim() == 3 else 1), x.shape[0], n, k
 
 
 def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, out_dtype=None,
@@ -209,33 +231,29 @@ def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, ou
     (or [n][k]), both bf16, f16, or int8 with x_scale [rows] and w_scale [groups][n] f32.
     out: [rows][n], by default of x's type (f32 for int8); rows of no group are not written.
     accumulate: out += (f32)."""
-    groups, rows, n, k = _operands(x, w, "x, w")
-    t = _TYPES.get(x.dtype, TYPE_F32)
-    if t == TYPE_F32 or x.shape[1] != k:
-        raise ValueError("x, w: expected [rows][k] and [groups][n][k], bf16, f16 or int8")
-    index = _device_of(x, "grouped_gemm")
+    groups, n, k = _matrices(w, "w")
+    dtype, shape = x.dtype, x.shape
+    t = _TYPES.get(dtype, TYPE_F32)
+    if len(shape) != 2 or shape[1] != k or t == TYPE_F32 or w.dtype is not dtype:
+        _refuse("x, w: expected [rows][k] and [groups][n][k] of one type, bf16, f16 or int8")
+    rows, index = shape[0], x.get_device()
+    if index < 0:
+        _refuse("grouped_gemm: expected CUDA tensors")
+    xs = ws = 0
+    if t == TYPE_INT8:
+        if x_scale is None or w_scale is None:
+            _refuse("int8: needs x_scale and w_scale")
+        xs = _vector(x_scale, rows, torch.float32, "x_scale", index)
+        ws = _vector(w_scale, groups * n, torch.float32, "w_scale", index)
+        dtype = torch.float32
+    elif x_scale is not None or w_scale is not None:
+        _refuse("x_scale, w_scale: for int8 only")
     off = _offsets(offsets, groups, index)
     x_ld = _row_stride(x, rows, k, "x", index)
     w_ld = _matrix_stride(w, groups, n, k, "w", index)
-    xs = ws = None
-    if t == TYPE_INT8:
-        if x_scale is None or w_scale is None:
-            raise ValueError("int8: needs x_scale and w_scale")
-        xs = _vector(x_scale, rows, torch.float32, "x_scale", index)
-        ws = _vector(w_scale, groups * n, torch.float32, "w_scale", index)
-    elif x_scale is not None or w_scale is not None:
-        raise ValueError("x_scale, w_scale: for int8 only")
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate: needs out")
-        if out_dtype is None:
-            out_dtype = torch.float32 if t == TYPE_INT8 else x.dtype
-        o = _out_type(None, None, out_dtype)
-        out = _new((rows, n), out_dtype, index, stream)
-    else:
-        o = _out_type(out, (rows, n), out_dtype)
-    io = GemmIO(groups, rows, n, k, t, o, 1 if accumulate else 0, off, x.data_ptr(), x_ld, xs, None, 0, w.data_ptr(), w_ld,
-                ws, out.data_ptr(), _row_stride(out, rows, n, "out", index))
+    out, o, o_ld = _output(out, (rows, n), dtype if out_dtype is None and out is None else out_dtype, accumulate, index, stream)
+    io = _pack_gemm(groups, rows, n, k, t, o, 1 if accumulate else 0, off, x.data_ptr(), x_ld, xs, 0, 0, w.data_ptr(), w_ld, ws,
+                    out.data_ptr(), o_ld)
     _enqueue(lib().nvfp4_moe_grouped_gemm, io, index, stream, "nvfp4_moe_grouped_gemm")
     return out
 
@@ -243,8 +261,8 @@ def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, ou
 def gemm_int8(x, w, x_scale, w_scale, *, out=None, out_dtype=None, accumulate: bool = False, stream=None):
     """out[t][j] = x_scale[t] * w_scale[j] * sum_k x[t][k] w[j][k], the sum exact. x: [rows][k]
     int8, w: [n][k] int8, scales f32. out: [rows][n], f32 by default. accumulate: out += (f32)."""
-    if x.dtype != torch.int8 or w.dim() != 2:
-        raise ValueError("x, w: expected int8 [rows][k] and [n][k]")
+    if x.dtype is not torch.int8 or w.dim() != 2:
+        _refuse("x, w: expected int8 [rows][k] and [n][k]")
     return grouped_gemm(x, w, None, x_scale=x_scale, w_scale=w_scale, out=out, out_dtype=out_dtype,
                         accumulate=accumulate, stream=stream)
 
@@ -252,24 +270,20 @@ def gemm_int8(x, w, x_scale, w_scale, *, out=None, out_dtype=None, accumulate: b
 def grouped_gemm_dx(dy, w, offsets=None, *, out=None, out_dtype=None, accumulate: bool = False, stream=None):
     """The gradient of grouped_gemm for x: dx[p] = dy[p] W_e. dy: [rows][n], w: [groups][n][k],
     both bf16 or f16. out: [rows][k], by default of dy's type; rows of no group are not written."""
-    groups, rows, n, k = _operands(dy, w, "dy, w")
-    t = _TYPES.get(dy.dtype, TYPE_F32)
-    if t not in (TYPE_BF16, TYPE_F16) or dy.shape[1] != n:
-        raise ValueError("dy, w: expected [rows][n] and [groups][n][k], bf16 or f16")
-    index = _device_of(dy, "grouped_gemm_dx")
+    groups, n, k = _matrices(w, "w")
+    dtype, shape = dy.dtype, dy.shape
+    t = _TYPES.get(dtype, TYPE_F32)
+    if len(shape) != 2 or shape[1] != n or (t != TYPE_BF16 and t != TYPE_F16) or w.dtype is not dtype:
+        _refuse("dy, w: expected [rows][n] and [groups][n][k] of one type, bf16 or f16")
+    rows, index = shape[0], dy.get_device()
+    if index < 0:
+        _refuse("grouped_gemm_dx: expected CUDA tensors")
     off = _offsets(offsets, groups, index)
     dy_ld = _row_stride(dy, rows, n, "dy", index)
     w_ld = _matrix_stride(w, groups, n, k, "w", index)
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate: needs out")
-        out_dtype = dy.dtype if out_dtype is None else out_dtype
-        o = _out_type(None, None, out_dtype)
-        out = _new((rows, k), out_dtype, index, stream)
-    else:
-        o = _out_type(out, (rows, k), out_dtype)
-    io = GemmIO(groups, rows, n, k, t, o, 1 if accumulate else 0, off, None, 0, None, dy.data_ptr(), dy_ld, w.data_ptr(), w_ld,
-                None, out.data_ptr(), _row_stride(out, rows, k, "out", index))
+    out, o, o_ld = _output(out, (rows, k), dtype if out_dtype is None and out is None else out_dtype, accumulate, index, stream)
+    io = _pack_gemm(groups, rows, n, k, t, o, 1 if accumulate else 0, off, 0, 0, 0, dy.data_ptr(), dy_ld, w.data_ptr(), w_ld, 0,
+                    out.data_ptr(), o_ld)
     _enqueue(lib().nvfp4_moe_grouped_gemm_dx, io, index, stream, "nvfp4_moe_grouped_gemm_dx")
     return out
 
@@ -278,25 +292,21 @@ def grouped_gemm_dw(dy, x, offsets=None, *, out=None, out_dtype=None, accumulate
     """The gradient of grouped_gemm for w: dW_e = sum over the rows p of e of dy[p]^T x[p].
     dy: [rows][n], x: [rows][k], both bf16 or f16. out: [groups][n][k] ([n][k] without
     offsets), f32 by default; zeros for a group without rows. accumulate: out += (f32)."""
-    t = _TYPES.get(dy.dtype, TYPE_F32)
-    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or dy.dtype != x.dtype or t not in (TYPE_BF16, TYPE_F16):
-        raise ValueError("dy, x: expected [rows][n] and [rows][k], both bf16 or f16")
-    index = _device_of(x, "grouped_gemm_dw")
-    (rows, k), n = x.shape, dy.shape[1]
+    dtype, shape, dy_shape = dy.dtype, x.shape, dy.shape
+    t = _TYPES.get(dtype, TYPE_F32)
+    if len(shape) != 2 or len(dy_shape) != 2 or dy_shape[0] != shape[0] or x.dtype is not dtype or (t != TYPE_BF16 and t != TYPE_F16):
+        _refuse("dy, x: expected [rows][n] and [rows][k] of one type, bf16 or f16")
+    rows, k = shape
+    n, index = dy_shape[1], x.get_device()
+    if index < 0:
+        _refuse("grouped_gemm_dw: expected CUDA tensors")
     groups = 1 if offsets is None else offsets.numel() - 1
     off = _offsets(offsets, groups, index)
     dy_ld = _row_stride(dy, rows, n, "dy", index)
     x_ld = _row_stride(x, rows, k, "x", index)
-    shape = (n, k) if offsets is None else (groups, n, k)
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate: needs out")
-        out_dtype = torch.float32 if out_dtype is None else out_dtype
-        o = _out_type(None, None, out_dtype)
-        out = _new(shape, out_dtype, index, stream)
-    else:
-        o = _out_type(out, shape, out_dtype)
-    io = GemmIO(groups, rows, n, k, t, o, 1 if accumulate else 0, off, x.data_ptr(), x_ld, None, dy.data_ptr(), dy_ld, None, 0,
-                None, out.data_ptr(), _matrix_stride(out, groups, n, k, "out", index))
+    out, o, o_ld = _output(out, (n, k) if offsets is None else (groups, n, k),
+                           torch.float32 if out_dtype is None and out is None else out_dtype, accumulate, index, stream)
+    io = _pack_gemm(groups, rows, n, k, t, o, 1 if accumulate else 0, off, x.data_ptr(), x_ld, 0, dy.data_ptr(), dy_ld, 0, 0, 0,
+                    out.data_ptr(), o_ld)
     _enqueue(lib().nvfp4_moe_grouped_gemm_dw, io, index, stream, "nvfp4_moe_grouped_gemm_dw")
     return out

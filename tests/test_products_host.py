@@ -120,6 +120,12 @@ def test_structures_match_the_header(tmp_path):
     for cls in (nv.QuantizeIO, nv.GemmIO):
         want += [C.sizeof(cls)] + [getattr(cls, f).offset for f, _ in cls._fields_]
     assert got == want
+    # the same layouts as the tensor calls pack them
+    import struct
+    assert [struct.calcsize("@4iPqPqP"), struct.calcsize("@7iPPqPPqPqPPq")] == [C.sizeof(nv.QuantizeIO), C.sizeof(nv.GemmIO)]
+    v = list(range(1, 19))
+    assert products._pack_gemm(*v) == bytes(nv.GemmIO(*v))
+    assert products._pack_quantize(*v[:9]) == bytes(nv.QuantizeIO(*v[:9]))
     assert (products.TYPE_BF16, products.TYPE_F16, products.TYPE_F32, products.TYPE_INT8) == (BF16, F16, F32, INT8)
 
 
