@@ -1,36 +1,31 @@
 // Rows to int8 codes and one FP32 scale per row, optionally of h = SiLU(gate) * up.
 //
-// scale = max|v| / 127 (FP32), q = the whole number nearest to the exact v / scale,
-// ties to the even one. v * (1 / scale) in FP32 is within 2^-16 of that quotient
-// (|quotient| <= 127 and two roundings of 2^-24 each), so rounding it is right unless
-// it stands within that of a half; only then is the quotient's side of the half taken
-// from the remainder v - q * scale, which one fused multiply-add gives exactly (it is a
-// whole multiple of the smaller ulp and at most about scale / 2, so it fits 24 bits).
+// scale = max|v| / 127 (FP32), q = the whole number nearest to the exact v / scale, ties to
+// the even one. q is rounded from v * (1 / scale), which may fall on the wrong side of a half;
+// the remainder d = v - q * scale tells: one fused multiply-add gives it exactly (it is a
+// whole multiple of the smaller ulp and at most about scale / 2, so it fits 24 bits), and q
+// is right wherever 2 |d| < scale. Only else is it corrected. That is no rare case with
+// 16-bit values: every v = max / 2 stands 63.5 steps of a rounded scale from zero.
 //
-// Bound by memory: every input value is read once and kept in registers, as FP32,
-// between the maximum and the rounding; a code costs one multiply, one add that leaves
-// the rounded number in the low bits, the distance to it, and its share of a byte
-// permute. A warp takes a row where there are rows enough to fill the GPU and the row
-// fits its registers, else the whole CTA does.
+// Bound by memory: every input is read once and waits in registers (16-bit values as they
+// are, h as FP32) between the maximum and the rounding. A code takes one multiply-add that
+// leaves the rounded number in the low bits of a float, one add that takes it out, one
+// multiply-add for d, two codes to an instruction, and the maximum of |d| over eight. A warp
+// takes a row where there are rows enough to fill the GPU, else a CTA does.
 #include "products.cuh"
 
 namespace nvmoe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunks = 8;              // chunks of 8 values that a thread keeps
 constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: v + kMagic holds rint(v) in its low bits
-constexpr float kNearHalf = 0.5f - 0x1p-15f;
 constexpr float kTiny = 0x1p-100f;
 
-// The code by the remainder: right for every finite v and scale > 0.
-__device__ __noinline__ int exact_code(float v, float scale) {
-    // Scales below 2^-100 and their values are brought up by 2^64, exactly: 1 / scale
-    // would overflow.
-    if (scale < kTiny) {
-        v *= 0x1p64f;
-        scale *= 0x1p64f;
-    }
+// The code for any finite v and scale > 0, for scales below kTiny: both are brought up by
+// 2^64, exactly (1 / scale would overflow).
+__device__ __noinline__ int tiny_code(float v, float scale) {
+    v *= 0x1p64f;
+    scale *= 0x1p64f;
     const float t = fminf(fmaxf(v / scale, -128.0f), 128.0f);   // a subnormal scale may be far off max|v| / 127
     if (fabsf(t) >= 127.5f) return t > 0.0f ? 127 : -127;
     float q = rintf(t);
@@ -39,56 +34,124 @@ __device__ __noinline__ int exact_code(float v, float scale) {
     return (int)fminf(fmaxf(q, -127.0f), 127.0f);
 }
 
-// Values c .. c+7 of a row as FP32 (zeros from cols on); kVec: p + c is 16-byte aligned.
-template <typename T, bool kVec>
-__device__ inline void load8(const T *p, int c, int cols, float (&v)[8]) {
-    if (kVec && c + 8 <= cols) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(p + c), b = *reinterpret_cast<const float4 *>(p + c + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4 *>(p + c);
-            const T *h = reinterpret_cast<const T *>(&a);
+__device__ inline float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ inline float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Eight values of a row as a thread keeps them: 16-bit ones as read, else FP32.
+template <typename T, bool kSwiglu>
+struct Chunk {
+    static constexpr bool kRaw = sizeof(T) == 2 && !kSwiglu;
+    uint32_t w[kRaw ? 4 : 8];
+    __device__ float2 pair(int i) const {
+        if constexpr (kRaw) {
+            const T *h = reinterpret_cast<const T *>(&w[i]);
+            return make_float2(to_f32(h[0]), to_f32(h[1]));
+        } else
+            return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    }
+    // Its largest magnitude, joined to m, as bits: NaN and infinities order above every
+    // number (of 16-bit values in both halves of m).
+    __device__ uint32_t top(uint32_t m) const {
+        if constexpr (kRaw) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = to_f32(h[j]);
+            for (int i = 0; i < 4; i++) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) m = max(m, w[i] & 0x7fffffffu);
+        }
+        return m;
+    }
+    // The largest magnitude of a thread's chunks as the bits of an FP32 number.
+    __device__ static uint32_t top_bits(uint32_t m) {
+        if constexpr (kRaw) {
+            m = max(m & 0xffffu, m >> 16);
+            const uint16_t h = (uint16_t)m;
+            return __float_as_uint(to_f32(*reinterpret_cast<const T *>(&h))) & 0x7fffffffu;
+        } else
+            return m;
+    }
+};
+
+// Values c .. c+7 as words (zeros from cols on); kVec: p + c is 16-byte aligned.
+template <typename T, bool kVec>
+__device__ inline void load8(const T *p, int c, int cols, uint32_t (&w)[sizeof(T) * 2]) {
+    if (kVec && c + 8 <= cols) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; i++) {
+            const uint4 a = *(reinterpret_cast<const uint4 *>(p + c) + i);
+            w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = c + j < cols ? to_f32(p[c + j]) : 0.0f;
+        for (int j = 0; j < 8; j++) {
+            if constexpr (sizeof(T) == 4)
+                w[j] = c + j < cols ? __float_as_uint(p[c + j]) : 0u;
+            else {
+                const uint32_t h = c + j < cols ? *reinterpret_cast<const uint16_t *>(p + c + j) : 0u;
+                w[j >> 1] = j & 1 ? w[j >> 1] | h << 16 : h;
+            }
+        }
     }
 }
 
 template <typename T, bool kSwiglu, bool kVec>
-__device__ inline void value8(const T *in, int c, int cols, float (&v)[8]) {
-    load8<T, kVec>(in, c, cols, v);
-    if (kSwiglu) {
-        float u[8];
-        load8<T, kVec>(in + cols, c, cols, u);
+__device__ inline void load_chunk(Chunk<T, kSwiglu> &k, const T *in, int c, int cols) {
+    if constexpr (!kSwiglu)
+        load8<T, kVec>(in, c, cols, k.w);
+    else {
+        Chunk<T, false> g, u;
+        load8<T, kVec>(in, c, cols, g.w);
+        load8<T, kVec>(in + cols, c, cols, u.w);
 #pragma unroll
-        for (int j = 0; j < 8; j++) v[j] = silu(v[j]) * u[j];
+        for (int i = 0; i < 4; i++) {
+            const float2 a = g.pair(i), b = u.pair(i);
+            k.w[2 * i] = __float_as_uint(silu(a.x) * b.x);
+            k.w[2 * i + 1] = __float_as_uint(silu(a.y) * b.y);
+        }
     }
 }
 
-template <bool kVec>
-__device__ inline void code8(const float (&v)[8], float scale, float inv, int8_t *q, int c, int cols) {
+template <typename T, bool kSwiglu, bool kVec>
+__device__ inline void code_chunk(const Chunk<T, kSwiglu> &k, float scale, float inv, int8_t *q, int c, int cols) {
     uint32_t r[8];
-    float far = 0.0f;
+    if (scale >= kTiny) {
+        float2 d[4];
+        float far = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const float t = v[j] * inv, m = t + kMagic;
-        r[j] = __float_as_uint(m);
-        far = fmaxf(far, fabsf(t - (m - kMagic)));
-    }
-    if (!(scale >= kTiny) || far > kNearHalf) {
-#pragma unroll 1
-        for (int j = 0; j < 8; j++) {
-            float vj = v[0];
+        for (int i = 0; i < 4; i++) {
+            const float2 v = k.pair(i), m = fma2(v, make_float2(inv, inv), make_float2(kMagic, kMagic));
+            const float2 n = add2(make_float2(kMagic, kMagic), make_float2(-m.x, -m.y));   // -q
+            d[i] = fma2(n, make_float2(scale, scale), v);
+            r[2 * i] = __float_as_uint(m.x);
+            r[2 * i + 1] = __float_as_uint(m.y);
+            far = fmaxf(far, fmaxf(fabsf(d[i].x), fabsf(d[i].y)));
+        }
+        if (2.0f * far >= scale) {
 #pragma unroll
-            for (int i = 1; i < 8; i++) vj = i == j ? v[i] : vj;
-            const int code = scale > 0.0f ? exact_code(vj, scale) : 0;
+            for (int j = 0; j < 8; j++) {
+                const float e = j & 1 ? d[j >> 1].y : d[j >> 1].x, e2 = 2.0f * fabsf(e);
+                if (e2 > scale || (e2 == scale && (r[j] & 1))) r[j] += e > 0.0f ? 1u : ~0u;
+            }
+        }
+    } else {
 #pragma unroll
-            for (int i = 0; i < 8; i++) r[i] = i == j ? (uint32_t)code : r[i];
+        for (int i = 0; i < 4; i++) {
+            const float2 v = k.pair(i);
+            r[2 * i] = scale > 0.0f ? (uint32_t)tiny_code(v.x, scale) : 0u;       // a scale of 0 or NaN: codes 0
+            r[2 * i + 1] = scale > 0.0f ? (uint32_t)tiny_code(v.y, scale) : 0u;
         }
     }
     if (kVec && c + 8 <= cols) {
@@ -103,9 +166,9 @@ __device__ inline void code8(const float (&v)[8], float scale, float inv, int8_t
     }
 }
 
-// kPer threads take a row (32 or kThreads). kKeep: its values stay in registers (cols
-// <= kPer * 8 * kChunks), else they are read twice.
-template <typename T, bool kSwiglu, bool kVec, int kPer, bool kKeep>
+// kPer threads take a row (32 or kThreads). kKeep chunks of it stay in a thread's registers
+// (cols <= kPer * 8 * kKeep); 0: the row is read twice.
+template <typename T, bool kSwiglu, bool kVec, int kPer, int kKeep>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const nvfp4_moe_quantize_io io) {
     __shared__ uint32_t part[kThreads / 32];
     const int row = kPer == 32 ? blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
@@ -115,25 +178,22 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const nvfp4_moe_quan
     const T *in = static_cast<const T *>(io.in) + (size_t)row * io.in_stride;
     int8_t *q = io.q + (size_t)row * io.q_stride;
 
-    float v[kKeep ? kChunks : 1][8];
-    uint32_t m = 0;   // max |v| as bits: NaN and infinities order above every number
+    Chunk<T, kSwiglu> v[kKeep ? kKeep : 1];
+    uint32_t m = 0;
     if (kKeep) {
 #pragma unroll
-        for (int i = 0; i < kChunks; i++)
-            if (8 * kPer * i < cols) value8<T, kSwiglu, kVec>(in, 8 * (kPer * i + me), cols, v[i]);
+        for (int i = 0; i < kKeep; i++)
+            if (8 * (kPer * i + me) < cols) load_chunk<T, kSwiglu, kVec>(v[i], in, 8 * (kPer * i + me), cols);
 #pragma unroll
-        for (int i = 0; i < kChunks; i++)
-            if (8 * kPer * i < cols)
-#pragma unroll
-                for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[i][j]) & 0x7fffffffu);
+        for (int i = 0; i < kKeep; i++)
+            if (8 * (kPer * i + me) < cols) m = v[i].top(m);
     } else {
         for (int c = 8 * me; c < cols; c += 8 * kPer) {
-            value8<T, kSwiglu, kVec>(in, c, cols, v[0]);
-#pragma unroll
-            for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[0][j]) & 0x7fffffffu);
+            load_chunk<T, kSwiglu, kVec>(v[0], in, c, cols);
+            m = v[0].top(m);
         }
     }
-    m = __reduce_max_sync(0xffffffffu, m);
+    m = __reduce_max_sync(0xffffffffu, Chunk<T, kSwiglu>::top_bits(m));
     if (kPer != 32) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
         __syncthreads();
@@ -145,27 +205,45 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const nvfp4_moe_quan
     if (me == 0) io.scale[row] = scale;
     if (kKeep) {
 #pragma unroll
-        for (int i = 0; i < kChunks; i++) {
+        for (int i = 0; i < kKeep; i++) {
             const int c = 8 * (kPer * i + me);
-            if (c < cols) code8<kVec>(v[i], scale, inv, q, c, cols);
+            if (c < cols) code_chunk<T, kSwiglu, kVec>(v[i], scale, inv, q, c, cols);
         }
     } else {
         for (int c = 8 * me; c < cols; c += 8 * kPer) {
-            value8<T, kSwiglu, kVec>(in, c, cols, v[0]);
-            code8<kVec>(v[0], scale, inv, q, c, cols);
+            load_chunk<T, kSwiglu, kVec>(v[0], in, c, cols);
+            code_chunk<T, kSwiglu, kVec>(v[0], scale, inv, q, c, cols);
         }
     }
 }
 
+template <typename T, bool kSwiglu, bool kVec, int kPer, int kKeep>
+void launch_as(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
+    const int grid = kPer == 32 ? cdiv(io.rows, kThreads / 32) : io.rows;
+    quantize_kernel<T, kSwiglu, kVec, kPer, kKeep><<<grid, kThreads, 0, s>>>(io);
+}
+
 template <typename T, bool kSwiglu, bool kVec>
 void launch(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
-    // A warp a row from four rows per SM up; fewer rows are done sooner by whole CTAs.
-    if (io.cols <= 32 * 8 * kChunks && io.rows >= 592)
-        quantize_kernel<T, kSwiglu, kVec, 32, true><<<cdiv(io.rows, kThreads / 32), kThreads, 0, s>>>(io);
-    else if (io.cols <= kThreads * 8 * kChunks)
-        quantize_kernel<T, kSwiglu, kVec, kThreads, true><<<io.rows, kThreads, 0, s>>>(io);
+    // A warp a row where there are rows enough to fill the GPU that way, else a CTA (us, warps /
+    // CTAs a row: 1000 x 768 BF16 2.3 / 2.2, 2048 x 768 2.6 / 3.3, 8192 x 768 6.3 / 10.5; 4096 x 2048
+    // 8.7 / 8.4, 32768 x 2048 35 / 50, FP32 55 / 60). h of more than 1024 columns takes too many
+    // registers of a warp (32768 x 2048 SwiGLU of BF16 125 / 67).
+    const int chunks = cdiv(io.cols, 8);
+    if (chunks <= 32 && io.rows >= 8)
+        launch_as<T, kSwiglu, kVec, 32, 1>(io, s);
+    else if (chunks <= 32 * 4 && io.rows >= 1536)
+        launch_as<T, kSwiglu, kVec, 32, 4>(io, s);
+    else if (!kSwiglu && chunks <= 32 * 8 && io.rows >= 8192)
+        launch_as<T, false, kVec, 32, 8>(io, s);
+    else if (chunks <= kThreads)
+        launch_as<T, kSwiglu, kVec, kThreads, 1>(io, s);
+    else if (chunks <= kThreads * 4)
+        launch_as<T, kSwiglu, kVec, kThreads, 4>(io, s);
+    else if (chunks <= kThreads * 8)
+        launch_as<T, kSwiglu, kVec, kThreads, 8>(io, s);
     else
-        quantize_kernel<T, kSwiglu, kVec, kThreads, false><<<io.rows, kThreads, 0, s>>>(io);
+        launch_as<T, kSwiglu, kVec, kThreads, 0>(io, s);
 }
 
 template <typename T>
