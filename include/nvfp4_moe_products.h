@@ -54,8 +54,10 @@ typedef enum {
 /* Largest k of an int8 product: (-128)^2 * k stays below 2^31, so that every sum of
  * products is exact in 32 bits. */
 #define NVFP4_MOE_INT8_MAX_K 131071
-/* Most groups of one product (experts of a layer). */
+/* Most groups of one product (experts of a layer), and the most rows, n, k or columns of
+ * a call (dw: groups * n too). */
 #define NVFP4_MOE_MAX_GROUPS 1024
+#define NVFP4_MOE_MAX_EXTENT (1 << 30)
 
 /* One quantiser call.
  *   rows, cols   rows >= 0 (0 is a no-op), cols >= 1 codes per row
@@ -63,7 +65,8 @@ typedef enum {
  *   swiglu       0: the row's values are v = in[row][0..cols)
  *                1: in rows hold gate | up, 2*cols values; v = SiLU(gate) * up in FP32
  *   in_stride    elements from one row to the next, >= the row's values
- *   q, q_stride  [rows][cols] int8, q_stride >= cols; bytes past cols are not written
+ *   q, q_stride  [rows][cols] int8, q_stride >= cols; bytes past cols are not written;
+ *                q must not overlap in
  *   scale        [rows] f32
  * scale = max|v| / 127 rounded to FP32; q = the whole number nearest to the exact
  * quotient v / scale (ties to the even one), clamped to +-127. A row whose scale is 0
@@ -103,8 +106,9 @@ NVFP4_MOE_API int nvfp4_moe_quantize_int8(const nvfp4_moe_quantize_io *io, void 
  *   out_type     BF16, F16 or F32; 16-bit sums are FP32, rounded once to out_type
  *   accumulate   nonzero: out += result, F32 outputs only
  * x, dy and w must be 16-byte aligned and their row strides a multiple of 16 bytes;
- * out needs its type's own alignment only. What a row holds between its length and its
- * stride is not used. dw writes zeros (or adds nothing) for an expert without rows. */
+ * out needs its type's own alignment only (16-byte aligned rows are faster) and must not
+ * overlap what the call reads. What a row holds between its length and its stride is
+ * neither used nor written. dw writes zeros (or adds nothing) for an expert without rows. */
 typedef struct {
     int32_t groups;
     int32_t rows;

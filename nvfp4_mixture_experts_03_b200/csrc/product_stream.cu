@@ -164,13 +164,10 @@ cudaError_t launch(const Product &p, nvfp4_moe_type out, cudaStream_t s) {
     // are no more than that; a dense call's rows in one batch up to 32.
     const int nt = p.groups > 1 || p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
     const dim3 grid(cdiv(p.n, kCols), p.offsets ? p.rows : cdiv(p.rows, 8 * nt));
-    if (nt == 1)
-        product_stream_kernel<T, 1><<<grid, kThreads, 0, s>>>(p, out);
-    else if (nt == 2)
-        product_stream_kernel<T, 2><<<grid, kThreads, 0, s>>>(p, out);
-    else
-        product_stream_kernel<T, 4><<<grid, kThreads, 0, s>>>(p, out);
-    return cudaGetLastError();
+    return launch_kernel(nt == 1   ? product_stream_kernel<T, 1>
+                         : nt == 2 ? product_stream_kernel<T, 2>
+                                   : product_stream_kernel<T, 4>,
+                         grid, kThreads, s, p, (int)out);
 }
 
 }  // namespace

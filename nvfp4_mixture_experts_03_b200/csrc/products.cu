@@ -34,7 +34,10 @@ int check_operand(const void *p, int64_t ld, int32_t cols, int es, int64_t matri
 int product(int mode, const nvfp4_moe_gemm_io *io, void *stream) {
     if (!io) return NVFP4_MOE_ERR_INVALID_ARG;
     if (io->groups < 1 || io->rows < 0 || io->n < 1 || io->k < 1) return NVFP4_MOE_ERR_INVALID_ARG;
-    if (io->groups > NVFP4_MOE_MAX_GROUPS) return NVFP4_MOE_ERR_UNSUPPORTED_DIMS;
+    // tensor-map coordinates are 32-bit, and a tile may start past the last row or column
+    if (io->groups > NVFP4_MOE_MAX_GROUPS || io->rows > NVFP4_MOE_MAX_EXTENT || io->n > NVFP4_MOE_MAX_EXTENT ||
+        io->k > NVFP4_MOE_MAX_EXTENT || (mode == kDw && (int64_t)io->groups * io->n > NVFP4_MOE_MAX_EXTENT))
+        return NVFP4_MOE_ERR_UNSUPPORTED_DIMS;
     const bool i8 = io->type == NVFP4_MOE_TYPE_INT8;
     if (!(is16(io->type) || (i8 && mode == kFwd)) || !floating(io->out_type)) return NVFP4_MOE_ERR_INVALID_ARG;
     if (io->accumulate && io->out_type != NVFP4_MOE_TYPE_F32) return NVFP4_MOE_ERR_INVALID_ARG;
@@ -52,7 +55,8 @@ int product(int mode, const nvfp4_moe_gemm_io *io, void *stream) {
     if (i8 && (!io->x_scale || !io->w_scale)) return NVFP4_MOE_ERR_INVALID_ARG;
     const int32_t out_cols = mode == kFwd ? io->n : io->k;
     if (!io->out || io->out_stride < out_cols) return NVFP4_MOE_ERR_INVALID_ARG;
-    if (io->out == io->x || io->out == io->dy || io->out == io->w) return NVFP4_MOE_ERR_INVALID_ARG;
+    if ((mode != kDx && io->out == io->x) || (mode != kFwd && io->out == io->dy) || (mode != kDw && io->out == io->w))
+        return NVFP4_MOE_ERR_INVALID_ARG;
     if (!aligned(io->out, size_of(io->out_type)) || !aligned(io->offsets, 4) ||
         (i8 && (!aligned(io->x_scale, 4) || !aligned(io->w_scale, 4))))
         return NVFP4_MOE_ERR_MISALIGNED;
@@ -87,7 +91,7 @@ extern "C" {
 int nvfp4_moe_quantize_int8(const nvfp4_moe_quantize_io *io, void *stream) {
     if (!io || io->rows < 0 || io->cols < 1) return NVFP4_MOE_ERR_INVALID_ARG;
     if (!floating(io->in_type) || (io->swiglu != 0 && io->swiglu != 1)) return NVFP4_MOE_ERR_INVALID_ARG;
-    if (io->cols > INT32_MAX / 2) return NVFP4_MOE_ERR_UNSUPPORTED_DIMS;
+    if (io->cols > NVFP4_MOE_MAX_EXTENT) return NVFP4_MOE_ERR_UNSUPPORTED_DIMS;
     if (io->rows == 0) return NVFP4_MOE_OK;
     if (!io->in || !io->q || !io->scale) return NVFP4_MOE_ERR_INVALID_ARG;
     if (io->in_stride < (int64_t)io->cols * (1 + io->swiglu) || io->q_stride < io->cols)

@@ -41,6 +41,16 @@ __device__ inline __half from_f32(float v) { return __float2half_rn(v); }
 template <>
 __device__ inline float from_f32(float v) { return v; }
 
+// A launch that reports its own error, and none that was pending before it.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 cudaError_t launch_quantize(const nvfp4_moe_quantize_io &io, cudaStream_t s);
 cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, nvfp4_moe_type out_type,
                                cudaStream_t s);

@@ -218,55 +218,49 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const nvfp4_moe_quan
 }
 
 template <typename T, bool kSwiglu, bool kVec, int kPer, int kKeep>
-void launch_as(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
+cudaError_t launch_as(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
     const int grid = kPer == 32 ? cdiv(io.rows, kThreads / 32) : io.rows;
-    quantize_kernel<T, kSwiglu, kVec, kPer, kKeep><<<grid, kThreads, 0, s>>>(io);
+    return launch_kernel(quantize_kernel<T, kSwiglu, kVec, kPer, kKeep>, dim3(grid), kThreads, s, io);
 }
 
 template <typename T, bool kSwiglu, bool kVec>
-void launch(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
+cudaError_t launch(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
     // A warp a row where there are rows enough to fill the GPU that way, else a CTA (us, warps /
     // CTAs a row: 1000 x 768 BF16 2.3 / 2.2, 2048 x 768 2.6 / 3.3, 8192 x 768 6.3 / 10.5; 4096 x 2048
     // 8.7 / 8.4, 32768 x 2048 35 / 50, FP32 55 / 60). h of more than 1024 columns takes too many
     // registers of a warp (32768 x 2048 SwiGLU of BF16 125 / 67).
     const int chunks = cdiv(io.cols, 8);
     if (chunks <= 32 && io.rows >= 8)
-        launch_as<T, kSwiglu, kVec, 32, 1>(io, s);
+        return launch_as<T, kSwiglu, kVec, 32, 1>(io, s);
     else if (chunks <= 32 * 4 && io.rows >= 1536)
-        launch_as<T, kSwiglu, kVec, 32, 4>(io, s);
+        return launch_as<T, kSwiglu, kVec, 32, 4>(io, s);
     else if (!kSwiglu && chunks <= 32 * 8 && io.rows >= 8192)
-        launch_as<T, false, kVec, 32, 8>(io, s);
+        return launch_as<T, false, kVec, 32, 8>(io, s);
     else if (chunks <= kThreads)
-        launch_as<T, kSwiglu, kVec, kThreads, 1>(io, s);
+        return launch_as<T, kSwiglu, kVec, kThreads, 1>(io, s);
     else if (chunks <= kThreads * 4)
-        launch_as<T, kSwiglu, kVec, kThreads, 4>(io, s);
+        return launch_as<T, kSwiglu, kVec, kThreads, 4>(io, s);
     else if (chunks <= kThreads * 8)
-        launch_as<T, kSwiglu, kVec, kThreads, 8>(io, s);
+        return launch_as<T, kSwiglu, kVec, kThreads, 8>(io, s);
     else
-        launch_as<T, kSwiglu, kVec, kThreads, 0>(io, s);
+        return launch_as<T, kSwiglu, kVec, kThreads, 0>(io, s);
 }
 
 template <typename T>
-void launch(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
+cudaError_t launch(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
     auto al = [](const void *p, int a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
     const bool vec = al(io.in, 16) && (io.rows == 1 || io.in_stride * sizeof(T) % 16 == 0) && al(io.q, 8) &&
                      (io.rows == 1 || io.q_stride % 8 == 0) && (!io.swiglu || (size_t)io.cols * sizeof(T) % 16 == 0);
-    if (io.swiglu)
-        vec ? launch<T, true, true>(io, s) : launch<T, true, false>(io, s);
-    else
-        vec ? launch<T, false, true>(io, s) : launch<T, false, false>(io, s);
+    if (io.swiglu) return vec ? launch<T, true, true>(io, s) : launch<T, true, false>(io, s);
+    return vec ? launch<T, false, true>(io, s) : launch<T, false, false>(io, s);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
-    if (io.in_type == NVFP4_MOE_TYPE_BF16)
-        launch<__nv_bfloat16>(io, s);
-    else if (io.in_type == NVFP4_MOE_TYPE_F16)
-        launch<__half>(io, s);
-    else
-        launch<float>(io, s);
-    return cudaGetLastError();
+    return io.in_type == NVFP4_MOE_TYPE_BF16  ? launch<__nv_bfloat16>(io, s)
+           : io.in_type == NVFP4_MOE_TYPE_F16 ? launch<__half>(io, s)
+                                              : launch<float>(io, s);
 }
 
 }  // namespace nvmoe

@@ -25,6 +25,7 @@ from . import OK, NVFP4MoEError, lib
 TYPE_BF16, TYPE_F16, TYPE_F32, TYPE_INT8 = 0, 1, 2, 3
 INT8_MAX_K = 131071
 MAX_GROUPS = 1024
+MAX_EXTENT = 1 << 30
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16, torch.float32: TYPE_F32, torch.int8: TYPE_INT8}
 
 

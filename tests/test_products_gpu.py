@@ -475,6 +475,156 @@ def test_values_outside_a_groups_rows_do_not_reach_it():
     assert torch.equal(got[2][1], want[2][1])
 
 
+def _check_all(x, dy, w, off, out_fwd, out_dx, out_dw, dw_dtype):
+    """All three products of one set of operands against 64 bits."""
+    n, k = w.shape[1:]
+    y, s = ref_fwd(x, w, off)
+    mine = ~y.isnan().any(1)
+    assert_within(out_fwd[mine], y[mine], tol16(k, s[mine], y[mine], out_fwd.dtype), "product")
+    y, s = ref_fwd(dy, w.transpose(1, 2), off)
+    assert_within(out_dx[mine], y[mine], tol16(n, s[mine], y[mine], out_dx.dtype), "dx")
+    for e, (lo, hi) in enumerate(zip(off[:-1], off[1:])):
+        ref, s = dy[lo:hi].double().T @ x[lo:hi].double(), dy[lo:hi].double().abs().T @ x[lo:hi].double().abs()
+        assert_within(out_dw[e], ref, tol16(max(hi - lo, 1), s, ref, dw_dtype), f"dw of {e}")
+
+
+@pytest.mark.parametrize("counts,n,k", [
+    ((3000,), 512, 512),                                   # whole pair tiles
+    ((1999, 0, 513, 70, 2), 576, 640),                     # ragged ones, 64-column boxes
+    ((700, 1300), 520, 1032),                              # columns that no 64 divides
+    ((257, 255, 256, 31, 33, 63, 65, 127, 129, 1), 768, 264),
+    ((5000, 1), 136, 2048), ((40,) * 60, 640, 256),
+])
+@pytest.mark.parametrize("dtype,wide", [(BF16, BF16), (F16, F32)])
+def test_large_tiles(counts, n, k, dtype, wide):
+    off, rows, E = offsets_of(counts), sum(counts), len(counts)
+    x, dy, w = normal((rows, k), dtype, 141), normal((rows, n), dtype, 142, 0.5), normal((E, n, k), dtype, 143, 0.1)
+    _check_all(x, dy, w, off.tolist(), nv.grouped_gemm(x, w, off, out_dtype=wide), nv.grouped_gemm_dx(dy, w, off, out_dtype=wide),
+               nv.grouped_gemm_dw(dy, x, off, out_dtype=wide), wide)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_outputs_with_rows_of_any_alignment(dtype):
+    """Outputs whose rows start anywhere, with what lies between and around them left alone."""
+    counts, n, k = (900, 3, 411), 517, 531
+    off, rows, E = offsets_of(counts, 2), sum(counts), len(counts)
+    x, dy, w = normal((rows + 5, k), BF16, 151), normal((rows + 5, n), BF16, 152), normal((E, n, k), BF16, 153, 0.1)
+    size = dtype.itemsize
+
+    def around(lead, cols):
+        buf = torch.full((lead * (cols + 4) + 1,), 7.0, dtype=dtype, device=DEV)
+        return buf, torch.as_strided(buf, (lead, cols), (cols + 4 if size == 4 else cols + 3, 1), 1)
+
+    bf, of = around(rows + 5, n)
+    bx, ox = around(rows + 5, k)
+    bw, ow = around(E * n, k)
+    nv.grouped_gemm(x, w, off, out=of)
+    nv.grouped_gemm_dx(dy, w, off, out=ox)
+    ow3 = torch.as_strided(bw, (E, n, k), (n * ow.stride(0), ow.stride(0), 1), 1)
+    nv.grouped_gemm_dw(dy, x, off, out=ow3)
+    _check_all(x, dy, w, off.tolist(), of, ox, ow3, dtype)
+    for buf, o, last in ((bf, of, rows + 2), (bx, ox, rows + 2), (bw, ow, E * n)):
+        written = torch.zeros_like(buf, dtype=torch.bool)
+        first = 0 if o is ow else 2
+        torch.as_strided(written, o.shape, o.stride(), 1)[first:last] = True
+        assert (buf[~written] == 7.0).all()
+
+
+@pytest.mark.parametrize("rows,n,k", [(6000, 200, 264), (20, 40, 72), (300, 264, 520)])
+def test_the_most_groups(rows, n, k):
+    """1024 groups, most of them small, some empty, one large."""
+    E = nv.products.MAX_GROUPS
+    p = torch.rand(E, generator=gen(161), device=DEV) ** 6
+    p[700] = 30.0
+    counts = torch.bincount(torch.multinomial(p, rows, replacement=True, generator=gen(162)), minlength=E).tolist()
+    off = offsets_of(counts)
+    x, dy, w = normal((rows, k), BF16, 163), normal((rows, n), BF16, 164, 0.5), normal((E, n, k), BF16, 165, 0.1)
+    _check_all(x, dy, w, off.tolist(), nv.grouped_gemm(x, w, off), nv.grouped_gemm_dx(dy, w, off),
+               nv.grouped_gemm_dw(dy, x, off, out_dtype=BF16), BF16)
+
+
+def test_int8_large_tiles():
+    counts, n, k = (1300, 0, 700, 31, 257), 520, 1040
+    off, rows, E = offsets_of(counts), sum(counts), len(counts)
+    x, w = codes((rows, k), 171), codes((E, n, k), 172)
+    xs, ws = torch.rand(rows, generator=gen(173), device=DEV) + 0.5, torch.rand(E, n, generator=gen(174), device=DEV) + 0.5
+    y, _ = ref_fwd(x, w, off.tolist())
+    for e, (lo, hi) in enumerate(zip(off.tolist()[:-1], off.tolist()[1:])):
+        y[lo:hi] *= xs[lo:hi, None].double() * ws[e].double()
+    for out_dtype in (F32, BF16, F16):
+        x_s = xs * (1e-4 if out_dtype == F16 else 1.0)
+        ref = y * (x_s / xs)[:, None].double()
+        got = nv.grouped_gemm(x, w, off, x_scale=x_s, w_scale=ws, out_dtype=out_dtype)
+        tol = 5 * 2.0 ** -24 * ref.abs() + (half_step(out_dtype, ref) * (1 + 2.0 ** -8) if out_dtype != F32 else 0)
+        assert_within(got, ref, tol, f"int8 to {out_dtype}")      # (x_s / xs rounds once more)
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """A fresh process whose first calls of the library run inside a capture, twice over the same buffers."""
+    import os
+    import subprocess
+    import sys
+    from conftest import ROOT
+    code = """
+import torch, nvfp4_mixture_experts_03_b200 as nv
+torch.manual_seed(0)
+x = torch.randn(300, 256, device="cuda", dtype=torch.bfloat16)
+w = torch.randn(4, 512, 256, device="cuda", dtype=torch.bfloat16)
+off = torch.tensor([0, 100, 100, 260, 300], device="cuda", dtype=torch.int32)
+torch.cuda.synchronize()
+def run():
+    q, s = nv.quantize_int8(x)
+    y = nv.grouped_gemm(x, w, off)
+    return [q, s, y, nv.grouped_gemm(x[:1], w[:1]), nv.grouped_gemm_dx(y, w, off), nv.grouped_gemm_dw(y, x, off)]
+g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+with torch.cuda.graph(g1):
+    a = run()
+with torch.cuda.graph(g2):
+    b = run()
+s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+for _ in range(5):
+    with torch.cuda.stream(s1):
+        g1.replay()
+    with torch.cuda.stream(s2):
+        g2.replay()
+torch.cuda.synchronize()
+c = run()
+for u, v, z in zip(a, b, c):
+    assert torch.equal(u, v) and torch.equal(u, z)
+assert nv.products_status() == 0
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
+
+
+def test_calls_from_several_threads():
+    import threading
+    run, _ = _all_calls(rows=200, n=264, k=328, seed=181)
+    want = run()
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(5):
+                got[i] = run(stream=s)
+            s.synchronize()
+        except Exception as e:      # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
+
+
 # --------------------------------------------------- together, as they are used
 
 def test_shared_expert_in_8_bits_beside_the_routed_layer():

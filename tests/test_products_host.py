@@ -38,6 +38,8 @@ def test_good_arguments_reach_the_device_check(which):
 
 GEMM_REFUSALS = [
     (dict(groups=0), INVALID, "all"), (dict(groups=-1), INVALID, "all"), (dict(groups=1025), DIMS, "all"),
+    (dict(rows=(1 << 30) + 1), DIMS, "all"), (dict(n=(1 << 30) + 1), DIMS, "all"), (dict(k=(1 << 30) + 1), DIMS, "all"),
+    (dict(n=1 << 29), DIMS, "dw"),                              # 4 * n rows of dw
     (dict(rows=-1), INVALID, "all"), (dict(n=0), INVALID, "all"), (dict(k=0), INVALID, "all"),
     (dict(type=F32), INVALID, "all"), (dict(type=7), INVALID, "all"), (dict(type=-1), INVALID, "all"),
     (dict(type=INT8), INVALID, "dx dw"),
@@ -57,7 +59,9 @@ GEMM_REFUSALS = [
     (dict(out=None), INVALID, "all"), (dict(out=BASE + 1), MISALIGNED, "all"),
     (dict(out=BASE + 2, out_type=F32), MISALIGNED, "all"),
     (dict(out_stride=60), INVALID, "all"), (dict(out_stride=95), INVALID, "fwd"),
-    (dict(out=BASE + (1 << 20)), INVALID, "all"),               # out is x
+    (dict(out=BASE + (1 << 20)), INVALID, "fwd dw"),            # out is x
+    (dict(out=BASE + (3 << 20)), INVALID, "dx dw"),             # out is dy
+    (dict(out=BASE + (4 << 20)), INVALID, "fwd dx"),            # out is w
     (dict(type=INT8, k=131072, x_stride=131072, w_stride=131072), DIMS, "fwd"),
     (dict(type=INT8, x_scale=None), INVALID, "fwd"), (dict(type=INT8, w_scale=None), INVALID, "fwd"),
     (dict(type=INT8, x_scale=BASE + 2), MISALIGNED, "fwd"), (dict(type=INT8, w_scale=BASE + 3), MISALIGNED, "fwd"),
@@ -92,7 +96,7 @@ def _quant(**over):
 @pytest.mark.parametrize("over,code", [
     (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(in_type=INT8), INVALID), (dict(in_type=5), INVALID),
     (dict(swiglu=2), INVALID), (dict(swiglu=1), INVALID),       # a stride of one row of values, not of gate | up
-    (dict(cols=1 << 30, in_stride=1 << 31, q_stride=1 << 30), DIMS),
+    (dict(cols=(1 << 30) + 1, in_stride=1 << 31, q_stride=1 << 31), DIMS),
     (dict(in_=None), INVALID), (dict(q=None), INVALID), (dict(scale=None), INVALID),
     (dict(in_stride=63), INVALID), (dict(q_stride=63), INVALID), (dict(q=BASE), INVALID),
     (dict(in_=BASE + 1), MISALIGNED), (dict(in_=BASE + 2, in_type=F32), MISALIGNED), (dict(scale=BASE + 2), MISALIGNED),
