@@ -78,7 +78,7 @@ def products_status(stream=None) -> int:
 
 _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stream().cuda_stream, without its object
-_empty = torch.empty
+_empty = torch.empty_strided   # half the time of torch.empty, and it pads rows without a view
 _UNIT = {torch.bfloat16: 8, torch.float16: 8, torch.float32: 4, torch.int8: 16}   # values in 16 bytes
 _pack_gemm = struct.Struct("@7iPPqPPqPqPPq").pack     # GemmIO
 _pack_quantize = struct.Struct("@4iPqPqP").pack       # QuantizeIO
@@ -170,10 +170,9 @@ def _new(shape, dtype, index: int, stream):
         with torch.cuda.stream(stream):
             return _new(shape, dtype, index, None)
     cols, unit = shape[-1], _UNIT[dtype]
-    if cols % unit == 0:
-        return _empty(shape, dtype=dtype, device=index), cols
     ld = -(-cols // unit) * unit
-    return _empty((*shape[:-1], ld), dtype=dtype, device=index)[..., :cols], ld
+    strides = (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1)
+    return _empty(shape, strides, dtype=dtype, device=index), ld
 
 
 def _enqueue(fn, io: bytes, index: int, stream, what: str) -> None:
@@ -216,10 +215,10 @@ def quantize_int8(x, *, swiglu: bool = False, q=None, scale=None, stream=None):
         s_ptr = _vector(scale, rows, torch.float32, "scale", index)
     else:
         if stream is None:
-            scale = _empty(rows, dtype=torch.float32, device=index)
+            scale = _empty((rows,), (1,), dtype=torch.float32, device=index)
         else:
             with torch.cuda.stream(stream):
-                scale = _empty(rows, dtype=torch.float32, device=index)
+                scale = _empty((rows,), (1,), dtype=torch.float32, device=index)
         s_ptr = scale.data_ptr()
     io = _pack_quantize(rows, cols, t, 1 if swiglu else 0, x.data_ptr(), x_ld, q.data_ptr(), q_ld, s_ptr)
     _enqueue(lib().nvfp4_moe_quantize_int8, io, index, stream, "nvfp4_moe_quantize_int8")
