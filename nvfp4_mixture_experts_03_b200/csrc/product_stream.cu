@@ -9,15 +9,16 @@
 // bits on every run.
 //
 // Bound by latency, then by memory: nothing is staged or laid out, no tensor map, no
-// barrier but the one before the join, and a warp's loads of a whole k range are in
-// flight before its first MMA waits.
+// barrier but the one before the join. Many warps with a few loads each in flight do better
+// than few with many (1 x 8192 x 8192 BF16: 19.7 us, 6.8 TB/s, with 2 pieces a lane and 4 CTAs an
+// SM; 26.0 with 4 pieces and 3 CTAs), as long as the loop that needs no masks has none.
 #include "products.cuh"
 
 namespace nvmoe {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kCols = 16;
-constexpr int kDeep = 4;   // 16-byte pieces of each row that a lane has in flight
+constexpr int kDeep = 2;   // 16-byte pieces of each row that a lane has in flight
 
 __device__ inline uint4 ld_stream(const void *p) {
     uint4 v;
@@ -28,14 +29,11 @@ __device__ inline uint4 ld_stream(const void *p) {
 }
 
 // Keeps the first n bytes of 16 (what a row holds past its length may be NaN).
-__device__ inline uint4 keep(uint4 v, int n) {
-    uint32_t *w = &v.x;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int b = n - 4 * i;
-        w[i] = b >= 4 ? w[i] : b <= 0 ? 0u : w[i] & ((1u << (8 * b)) - 1);
-    }
-    return v;
+__device__ inline void keep(uint4 &v, int n) {
+    v.x &= n >= 4 ? ~0u : (1u << (8 * max(n, 0))) - 1;
+    v.y &= n >= 8 ? ~0u : (1u << (8 * max(n - 4, 0))) - 1;
+    v.z &= n >= 12 ? ~0u : (1u << (8 * max(n - 8, 0))) - 1;
+    v.w &= n >= 16 ? ~0u : (1u << (8 * max(n - 12, 0))) - 1;
 }
 
 __device__ inline void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
@@ -61,7 +59,7 @@ __device__ inline void put(O *o, float v, bool add) {
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(kThreads) product_stream_kernel(const __grid_constant__ Product p, const int out_type) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) product_stream_kernel(const __grid_constant__ Product p, const int out_type) {
     constexpr bool kI8 = std::is_same<T, int8_t>::value;
     using Acc = typename std::conditional<kI8, int32_t, float>::type;
     __shared__ Acc part[kWarps][8 * NT][kCols + 1];
@@ -89,43 +87,21 @@ __global__ void __launch_bounds__(kThreads) product_stream_kernel(const __grid_c
     const int nrow = min(8 * NT, end - row0);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const int64_t kb = (int64_t)p.k * sizeof(T);   // bytes of a row
+    const uint32_t kb = (uint32_t)p.k * sizeof(T);   // bytes of a row
     const int64_t w_ld = p.w_ld * sizeof(T), x_ld = p.x_ld * sizeof(T);
+    // 64 bytes of every row a piece, 64 * kDeep bytes a step; the warps take steps in turn.
+    constexpr uint32_t kStepBytes = 64 * kDeep, kRound = kWarps * kStepBytes;
+    const uint32_t first = warp * kStepBytes + 16 * q;
     // Rows past the matrix or the batch repeat its last one; their results are dropped.
-    const char *w0 = static_cast<const char *>(p.w) + ((int64_t)e * p.n + min(col0 + g, p.n - 1)) * w_ld;
-    const char *w1 = static_cast<const char *>(p.w) + ((int64_t)e * p.n + min(col0 + g + 8, p.n - 1)) * w_ld;
+    const char *w0 = static_cast<const char *>(p.w) + ((int64_t)e * p.n + min(col0 + g, p.n - 1)) * w_ld + first;
+    const char *w1 = static_cast<const char *>(p.w) + ((int64_t)e * p.n + min(col0 + g + 8, p.n - 1)) * w_ld + first;
     const char *x[NT];
 #pragma unroll
-    for (int t = 0; t < NT; t++) x[t] = static_cast<const char *>(p.x) + (int64_t)(row0 + min(8 * t + g, nrow - 1)) * x_ld;
+    for (int t = 0; t < NT; t++) x[t] = static_cast<const char *>(p.x) + (int64_t)(row0 + min(8 * t + g, nrow - 1)) * x_ld + first;
 
     Acc acc[NT][4] = {};
-    // 64 bytes of every row a piece, 64 * kDeep bytes a step; the warps take steps in turn.
-    for (int64_t k0 = (int64_t)warp * (64 * kDeep); k0 < kb; k0 += kWarps * 64 * kDeep) {
-        uint4 a0[kDeep], a1[kDeep], b[NT][kDeep];
-#pragma unroll
-        for (int d = 0; d < kDeep; d++) {
-            const int64_t at = k0 + 64 * d + 16 * q;
-            if (at < kb) {
-                a0[d] = ld_stream(w0 + at);
-                a1[d] = ld_stream(w1 + at);
-#pragma unroll
-                for (int t = 0; t < NT; t++) b[t][d] = *reinterpret_cast<const uint4 *>(x[t] + at);
-            } else {
-                a0[d] = a1[d] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int t = 0; t < NT; t++) b[t][d] = make_uint4(0, 0, 0, 0);
-            }
-        }
-        if (k0 + 64 * kDeep > kb) {
-#pragma unroll
-            for (int d = 0; d < kDeep; d++) {
-                const int left = (int)max((int64_t)0, min((int64_t)16, kb - (k0 + 64 * d + 16 * q)));
-                a0[d] = keep(a0[d], left);
-                a1[d] = keep(a1[d], left);
-#pragma unroll
-                for (int t = 0; t < NT; t++) b[t][d] = keep(b[t][d], left);
-            }
-        }
+    uint4 a0[kDeep], a1[kDeep], b[NT][kDeep];
+    auto products = [&]() {
 #pragma unroll
         for (int d = 0; d < kDeep; d++)
 #pragma unroll
@@ -133,6 +109,40 @@ __global__ void __launch_bounds__(kThreads) product_stream_kernel(const __grid_c
                 mma16(acc[t], a0[d].x, a1[d].x, a0[d].y, a1[d].y, b[t][d].x, b[t][d].y, T());
                 mma16(acc[t], a0[d].z, a1[d].z, a0[d].w, a1[d].w, b[t][d].z, b[t][d].w, T());
             }
+    };
+    uint32_t k0 = warp * kStepBytes;
+    for (; k0 + kStepBytes <= kb; k0 += kRound) {
+#pragma unroll
+        for (int d = 0; d < kDeep; d++) {
+            a0[d] = ld_stream(w0 + 64 * d);
+            a1[d] = ld_stream(w1 + 64 * d);
+#pragma unroll
+            for (int t = 0; t < NT; t++) b[t][d] = *reinterpret_cast<const uint4 *>(x[t] + 64 * d);
+        }
+        w0 += kRound;
+        w1 += kRound;
+#pragma unroll
+        for (int t = 0; t < NT; t++) x[t] += kRound;
+        products();
+    }
+    if (k0 < kb) {   // one warp's last step: zeros past the rows' ends
+        const int left = (int)(kb - k0) - 16 * q;   // bytes from this lane's first
+#pragma unroll
+        for (int d = 0; d < kDeep; d++) {
+            const int n = left - 64 * d;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            a0[d] = n > 0 ? ld_stream(w0 + 64 * d) : zero;
+            a1[d] = n > 0 ? ld_stream(w1 + 64 * d) : zero;
+#pragma unroll
+            for (int t = 0; t < NT; t++) b[t][d] = n > 0 ? *reinterpret_cast<const uint4 *>(x[t] + 64 * d) : zero;
+            if (n > 0 && n < 16) {
+                keep(a0[d], n);
+                keep(a1[d], n);
+#pragma unroll
+                for (int t = 0; t < NT; t++) keep(b[t][d], n);
+            }
+        }
+        products();
     }
 #pragma unroll
     for (int t = 0; t < NT; t++)
@@ -174,17 +184,17 @@ cudaError_t launch(const Product &p, nvfp4_moe_type out, cudaStream_t s) {
 
 // Streaming reads a group's matrix again for every batch of its rows, and has a CTA for every
 // 16 columns of each; the tensor-core tiles have some 6 us of start and end. Measured against
-// them (us, streamed / tiles): dense 8 x 8192 x 8192 BF16 26 / 31, 16 x the same 42 / 32, 64 x
-// 1536 x 2048 8.6 / 10.2, 64 x 2560 x 2560 14.6 / 11.5, 512 x 256 x 256 4.2 / 6.1, 32 x 8192 x 256
-// 6.8 / 6.1; by group 32 rows of 8 x 256 x 256 3.3 / 6.5, 64 of 16 x 512 x 512 7.4 / 7.1, 10 of 64 x
-// 1536 x 2048 11.5 / 12.1, 32 of the same 32.6 / 28.6.
+// them (us, streamed / tiles, BF16): dense 8 x 8192 x 8192 20 / 30, 32 x the same 35 / 31, 64 x 1536 x
+// 2048 6.5 / 10.6, 64 x 2560 x 2560 10.7 / 12.0, 128 x 2048 x 768 7.4 / 7.5, 201 x the same 11.1 / 7.6, 32 x
+// 8192 x 256 5.0 / 6.1, 64 x the same 8.4 / 6.1; by group 32 rows of 8 x 1536 x 2048 10.5 / 10.7, 64 of
+// them 15.4 / 10.7, 32 of 64 x 1536 x 2048 27 / 34, 64 of 16 x 512 x 512 5.5 / 7.2, 128 of them 8.1 / 7.2.
 bool product_streams(int mode, const Product &p, int elem_bytes) {
     if (mode != kFwd) return false;
     const int64_t blocks = cdiv(p.n, kCols);
-    if (p.offsets) return p.rows * blocks <= 1536;
+    if (p.offsets) return p.rows * blocks <= 3072;
     if (p.rows <= 8) return true;
     const int64_t passes = cdiv(p.rows, 32);
-    return passes * blocks <= 296 && passes * p.n * p.k * elem_bytes <= 14000000;
+    return passes * blocks <= 512 && passes * p.n * p.k * elem_bytes <= 30000000;
 }
 
 cudaError_t launch_product_stream(const Product &p, nvfp4_moe_type type, nvfp4_moe_type out, cudaStream_t s) {
