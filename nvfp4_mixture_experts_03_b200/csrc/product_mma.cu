@@ -51,7 +51,7 @@ struct MmaParams {
     Product p;
     uint32_t idesc;        // instruction descriptor without its N
     int32_t out_type;
-    int32_t bn;            // most rows of a tile (N); a multiple of 64 per CTA for dw
+    int32_t bn, bn_log2;   // most rows of a tile (N): 64, 128 or 256
     int32_t box;           // rows of the larger K-major B box
     int32_t stages;
     int32_t staged;        // whole batches of outputs leave as boxes (map_o is set); rows are 16-byte aligned
@@ -277,10 +277,11 @@ template <int MODE, int CG>
 struct Tiles {
     const MmaParams &q;
     const Groups &g;
-    int mt, rt, total;   // column tiles, row tiles (dw: of all groups), all tiles
+    int mt, rt, nt, total;   // column tiles, row tiles (dw: of all groups, and of each), all tiles
     __device__ Tiles(const MmaParams &q_, const Groups &g_) : q(q_), g(g_) {
-        mt = cdiv(MODE == kFwd ? q.p.n : q.p.k, 128 * CG);
-        rt = MODE == kDw ? q.p.groups * cdiv(q.p.n, q.bn) : g.before[q.p.groups];
+        mt = ((MODE == kFwd ? q.p.n : q.p.k) + 128 * CG - 1) / (128 * CG);
+        nt = (q.p.n + q.bn - 1) >> q.bn_log2;
+        rt = MODE == kDw ? q.p.groups * nt : g.before[q.p.groups];
         total = mt * rt;
     }
     // Tile i, by a whole warp. Tiles run down kBand row tiles before they step to the next
@@ -289,11 +290,11 @@ struct Tiles {
     __device__ OutTile at(int i) const {
         OutTile t;
         const int lane = threadIdx.x & 31;
-        const int band = i / (kBand * mt), j = i - band * kBand * mt, high = min(kBand, rt - band * kBand);
-        const int r = band * kBand + j % high;
-        t.m0 = j / high * 128 * CG;
+        const int band = i / (kBand * mt), j = i - band * kBand * mt, high = rt - band * kBand;
+        const int m = high >= kBand ? j / kBand : j / high;
+        const int r = band * kBand + j - m * min(kBand, high);
+        t.m0 = m * 128 * CG;
         if (MODE == kDw) {
-            const int nt = cdiv(q.p.n, q.bn);
             const int at = r / nt;
             t.e = g.before[at] & 1023;
             t.row0 = (r - at * nt) * q.bn;
@@ -308,7 +309,7 @@ struct Tiles {
             t.e = 32 * hi + __popc(__ballot_sync(0xffffffffu, c < E && g.before[min(c, E)] <= r)) - 1;
             // the group's rows in equal tiles, whole multiples of 16 per CTA
             const int n = g.before[t.e + 1] - g.before[t.e], cnt = g.lo[t.e + 1] - g.lo[t.e];
-            const int each = cdiv(cdiv(cnt, n), 16 * CG) * 16 * CG, first = (r - g.before[t.e]) * each;
+            const int each = ((n == 1 ? cnt : cdiv(cnt, n)) + 16 * CG - 1) / (16 * CG) * (16 * CG), first = (r - g.before[t.e]) * each;
             t.row0 = g.lo[t.e] + first;
             t.nrow = max(0, min(each, cnt - first));
             t.c0 = 0;
@@ -361,14 +362,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&map_a);
         tma_prefetch_desc(&map_b);
     }
-    {   // The groups' rows and row tiles, four groups a thread: offsets clamped into the
+    if (!q.p.offsets) {   // one group of all rows
+        if (threadIdx.x == 0) {
+            groups->lo[0] = groups->before[0] = 0;
+            groups->lo[1] = q.p.rows;
+            groups->before[1] = (q.p.rows + q.bn - 1) >> q.bn_log2;
+        }
+    } else {
+        // The groups' rows and row tiles, four groups a thread: offsets clamped into the
         // rows and to no less than those before them (a running maximum), then summed.
         constexpr int kPer = NVFP4_MOE_MAX_GROUPS / kScanThreads;
         const int E = q.p.groups, e0 = kPer * threadIdx.x;
         int off[kPer + 1], top = 0;
 #pragma unroll
         for (int i = 0; i <= kPer; i++) {
-            off[i] = e0 + i > E ? 0 : q.p.offsets ? min(max(q.p.offsets[e0 + i], 0), q.p.rows) : e0 + i ? q.p.rows : 0;
+            off[i] = e0 + i > E ? 0 : min(max(q.p.offsets[e0 + i], 0), q.p.rows);
             top = max(top, off[i]);
         }
 #pragma unroll
@@ -377,14 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         int run = __shfl_up_sync(0xffffffffu, top, 1);
         if (lane == 0) run = 0;
-        for (int w = 0; w < warp; w++) run = max(run, groups->warp_max[w]);
+        run = max(run, __reduce_max_sync(0xffffffffu, lane < warp ? groups->warp_max[lane] : 0));
         int tiles[kPer], sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             run = max(run, off[i]);
             const int count = max(off[i + 1] - run, 0);
             if (e0 + i <= E) groups->lo[e0 + i] = run;
-            tiles[i] = e0 + i < E ? cdiv(count, q.bn) : 0;
+            tiles[i] = e0 + i < E ? (count + q.bn - 1) >> q.bn_log2 : 0;
             sum += tiles[i];
         }
         int upto = sum;
@@ -395,8 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 31) groups->warp_sum[warp] = upto;
         __syncthreads();
-        upto -= sum;
-        for (int w = 0; w < warp; w++) upto += groups->warp_sum[w];
+        upto += __reduce_add_sync(0xffffffffu, lane < warp ? groups->warp_sum[lane] : 0) - sum;
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             if (MODE != kDw && e0 + i <= E) groups->before[e0 + i] = upto;
@@ -959,6 +966,7 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     const Shape shape = choose(mode, p, i8, cols, r);
     const int cg = shape.cg;
     q.bn = shape.bn;
+    q.bn_log2 = q.bn == 64 ? 6 : q.bn == 128 ? 7 : 8;
     q.box = std::min(128, q.bn / cg);
     q.stages = (int)std::min<size_t>(kMaxStages, (kSmemLimit - smem_bytes(q.bn, cg, 0)) / stage_bytes(q.bn, cg));
     // D F32 (or S32), A and B F16, BF16 or S8, their majors, M
