@@ -95,46 +95,42 @@ def _vector(t, n: int, dtype, name: str, index: int) -> int:
     return t.data_ptr()
 
 
-def _row_stride(t, rows: int, cols: int, name: str, index: int) -> int:
-    """The row stride of [rows][cols] with contiguous rows."""
-    if t.get_device() != index:
-        _refuse(f"{name}: expected a tensor on cuda:{index}")
-    ld, step = t.stride()
-    if step != 1 and cols != 1:
-        _refuse(f"{name}: expected contiguous rows")
+def _rows(t, index: int, name: str):
+    """(rows, cols, row stride) of a matrix with contiguous rows."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.get_device() != index or (stride[1] != 1 and shape[1] != 1):
+        _refuse(f"{name}: expected a matrix with contiguous rows on cuda:{index}")
+    rows, cols = shape
     if rows > 1:
-        return ld
+        return rows, cols, stride[0]
     unit = _UNIT[t.dtype]
-    return -(-cols // unit) * unit   # one row: no stride to take
+    return rows, cols, -(-cols // unit) * unit   # one row: no stride to take
 
 
-def _matrix_stride(t, groups: int, n: int, k: int, name: str, index: int) -> int:
-    """The row stride of [groups][n][k] or [n][k] whose matrices follow one another."""
+def _matrices(t, index: int, name: str):
+    """(groups, n, k, row stride) of [groups][n][k] or [n][k] whose matrices follow one another."""
+    shape, stride = t.shape, t.stride()
     if t.get_device() != index:
         _refuse(f"{name}: expected a tensor on cuda:{index}")
-    stride = t.stride()
+    if len(shape) == 2:
+        n, k = shape
+        groups, ld = 1, stride[0]
+    elif len(shape) == 3:
+        groups, n, k = shape
+        ld = stride[1]
+        if groups > 1:
+            if n == 1:
+                ld = stride[0]
+            elif stride[0] != n * ld:
+                _refuse(f"{name}: matrices have to follow one another, n rows apart")
+    else:
+        _refuse(f"{name}: expected [groups][n][k] or [n][k]")
     if stride[-1] != 1 and k != 1:
         _refuse(f"{name}: expected contiguous rows")
-    if n > 1:
-        ld = stride[-2]
-    elif groups > 1:
-        ld = stride[0]
-    else:
+    if n <= 1 and groups <= 1:
         unit = _UNIT[t.dtype]
         ld = -(-k // unit) * unit
-    if groups > 1 and stride[0] != n * ld:
-        _refuse(f"{name}: matrices have to follow one another, n rows apart")
-    return ld
-
-
-def _matrices(w, name: str):
-    """(groups, n, k) of [groups][n][k] or [n][k]."""
-    shape = w.shape
-    if len(shape) == 3:
-        return shape
-    if len(shape) != 2:
-        _refuse(f"{name}: expected [groups][n][k] or [n][k]")
-    return 1, shape[0], shape[1]
+    return groups, n, k, ld
 
 
 def _offsets(offsets, groups: int, index: int) -> int:
@@ -159,9 +155,7 @@ def _output(out, shape, dtype, accumulate: bool, index: int, stream):
     t = _TYPES.get(out.dtype, TYPE_INT8)
     if t == TYPE_INT8 or tuple(out.shape) != tuple(shape) or (dtype is not None and out.dtype != dtype):
         _refuse(f"out: expected {list(shape)} of {dtype or 'bf16, f16 or f32'}")
-    if len(shape) == 3:
-        return out, t, _matrix_stride(out, *shape, "out", index)
-    return out, t, _row_stride(out, *shape, "out", index)
+    return out, t, (_matrices if len(shape) == 3 else _rows)(out, index, "out")[-1]
 
 
 def _new(shape, dtype, index: int, stream):
@@ -191,14 +185,10 @@ def quantize_int8(x, *, swiglu: bool = False, q=None, scale=None, stream=None):
     nearest whole number (ties to even). x: [rows][cols] bf16, f16 or f32; with `swiglu`
     [rows][2*cols] holding gate | up, and v = SiLU(gate) * up.
     Returns (q int8 [rows][cols], scale f32 [rows])."""
-    t, shape = _TYPES.get(x.dtype, TYPE_INT8), x.shape
-    if len(shape) != 2 or t == TYPE_INT8:
-        _refuse("x: expected [rows][cols] bf16, f16 or f32")
-    rows, cols = shape
-    index = x.get_device()
-    if index < 0:
-        _refuse("quantize_int8: expected CUDA tensors")
-    x_ld = _row_stride(x, rows, cols, "x", index)
+    t, index = _TYPES.get(x.dtype, TYPE_INT8), x.get_device()
+    if t == TYPE_INT8 or index < 0:
+        _refuse("quantize_int8: expected a CUDA tensor [rows][cols], bf16, f16 or f32")
+    rows, cols, x_ld = _rows(x, index, "x")
     if swiglu:
         if cols % 2:
             _refuse("x: gate | up are an even number of values")
@@ -207,10 +197,10 @@ def quantize_int8(x, *, swiglu: bool = False, q=None, scale=None, stream=None):
         _refuse("x: expected at least one value a row")
     if q is None:
         q, q_ld = _new((rows, cols), torch.int8, index, stream)
-    elif q.dtype != torch.int8 or tuple(q.shape) != (rows, cols):
-        _refuse(f"q: expected int8 [{rows}][{cols}]")
     else:
-        q_ld = _row_stride(q, rows, cols, "q", index)
+        if q.dtype is not torch.int8 or tuple(q.shape) != (rows, cols):
+            _refuse(f"q: expected int8 [{rows}][{cols}]")
+        q_ld = _rows(q, index, "q")[2]
     if scale is not None:
         s_ptr = _vector(scale, rows, torch.float32, "scale", index)
     else:
@@ -231,14 +221,14 @@ def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, ou
     (or [n][k]), both bf16, f16, or int8 with x_scale [rows] and w_scale [groups][n] f32.
     out: [rows][n], by default of x's type (f32 for int8); rows of no group are not written.
     accumulate: out += (f32)."""
-    groups, n, k = _matrices(w, "w")
-    dtype, shape = x.dtype, x.shape
+    dtype, index = x.dtype, x.get_device()
     t = _TYPES.get(dtype, TYPE_F32)
-    if len(shape) != 2 or shape[1] != k or t == TYPE_F32 or w.dtype is not dtype:
-        _refuse("x, w: expected [rows][k] and [groups][n][k] of one type, bf16, f16 or int8")
-    rows, index = shape[0], x.get_device()
-    if index < 0:
-        _refuse("grouped_gemm: expected CUDA tensors")
+    if index < 0 or t == TYPE_F32 or w.dtype is not dtype:
+        _refuse("grouped_gemm: expected CUDA tensors of one type, bf16, f16 or int8")
+    rows, cols, x_ld = _rows(x, index, "x")
+    groups, n, k, w_ld = _matrices(w, index, "w")
+    if cols != k:
+        _refuse(f"x, w: rows of {cols} and of {k} values")
     xs = ws = 0
     if t == TYPE_INT8:
         if x_scale is None or w_scale is None:
@@ -249,9 +239,9 @@ def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, ou
     elif x_scale is not None or w_scale is not None:
         _refuse("x_scale, w_scale: for int8 only")
     off = _offsets(offsets, groups, index)
-    x_ld = _row_stride(x, rows, k, "x", index)
-    w_ld = _matrix_stride(w, groups, n, k, "w", index)
-    out, o, o_ld = _output(out, (rows, n), dtype if out_dtype is None and out is None else out_dtype, accumulate, index, stream)
+    if out is None and out_dtype is None:
+        out_dtype = dtype
+    out, o, o_ld = _output(out, (rows, n), out_dtype, accumulate, index, stream)
     io = _pack_gemm(groups, rows, n, k, t, o, 1 if accumulate else 0, off, x.data_ptr(), x_ld, xs, 0, 0, w.data_ptr(), w_ld, ws,
                     out.data_ptr(), o_ld)
     _enqueue(lib().nvfp4_moe_grouped_gemm, io, index, stream, "nvfp4_moe_grouped_gemm")
@@ -270,18 +260,18 @@ def gemm_int8(x, w, x_scale, w_scale, *, out=None, out_dtype=None, accumulate: b
 def grouped_gemm_dx(dy, w, offsets=None, *, out=None, out_dtype=None, accumulate: bool = False, stream=None):
     """The gradient of grouped_gemm for x: dx[p] = dy[p] W_e. dy: [rows][n], w: [groups][n][k],
     both bf16 or f16. out: [rows][k], by default of dy's type; rows of no group are not written."""
-    groups, n, k = _matrices(w, "w")
-    dtype, shape = dy.dtype, dy.shape
+    dtype, index = dy.dtype, dy.get_device()
     t = _TYPES.get(dtype, TYPE_F32)
-    if len(shape) != 2 or shape[1] != n or (t != TYPE_BF16 and t != TYPE_F16) or w.dtype is not dtype:
-        _refuse("dy, w: expected [rows][n] and [groups][n][k] of one type, bf16 or f16")
-    rows, index = shape[0], dy.get_device()
-    if index < 0:
-        _refuse("grouped_gemm_dx: expected CUDA tensors")
+    if index < 0 or t > TYPE_F16 or w.dtype is not dtype:
+        _refuse("grouped_gemm_dx: expected CUDA tensors of one type, bf16 or f16")
+    rows, cols, dy_ld = _rows(dy, index, "dy")
+    groups, n, k, w_ld = _matrices(w, index, "w")
+    if cols != n:
+        _refuse(f"dy, w: rows of {cols} values and matrices of {n} rows")
     off = _offsets(offsets, groups, index)
-    dy_ld = _row_stride(dy, rows, n, "dy", index)
-    w_ld = _matrix_stride(w, groups, n, k, "w", index)
-    out, o, o_ld = _output(out, (rows, k), dtype if out_dtype is None and out is None else out_dtype, accumulate, index, stream)
+    if out is None and out_dtype is None:
+        out_dtype = dtype
+    out, o, o_ld = _output(out, (rows, k), out_dtype, accumulate, index, stream)
     io = _pack_gemm(groups, rows, n, k, t, o, 1 if accumulate else 0, off, 0, 0, 0, dy.data_ptr(), dy_ld, w.data_ptr(), w_ld, 0,
                     out.data_ptr(), o_ld)
     _enqueue(lib().nvfp4_moe_grouped_gemm_dx, io, index, stream, "nvfp4_moe_grouped_gemm_dx")
@@ -292,20 +282,19 @@ def grouped_gemm_dw(dy, x, offsets=None, *, out=None, out_dtype=None, accumulate
     """The gradient of grouped_gemm for w: dW_e = sum over the rows p of e of dy[p]^T x[p].
     dy: [rows][n], x: [rows][k], both bf16 or f16. out: [groups][n][k] ([n][k] without
     offsets), f32 by default; zeros for a group without rows. accumulate: out += (f32)."""
-    dtype, shape, dy_shape = dy.dtype, x.shape, dy.shape
+    dtype, index = x.dtype, x.get_device()
     t = _TYPES.get(dtype, TYPE_F32)
-    if len(shape) != 2 or len(dy_shape) != 2 or dy_shape[0] != shape[0] or x.dtype is not dtype or (t != TYPE_BF16 and t != TYPE_F16):
-        _refuse("dy, x: expected [rows][n] and [rows][k] of one type, bf16 or f16")
-    rows, k = shape
-    n, index = dy_shape[1], x.get_device()
-    if index < 0:
-        _refuse("grouped_gemm_dw: expected CUDA tensors")
+    if index < 0 or t > TYPE_F16 or dy.dtype is not dtype:
+        _refuse("grouped_gemm_dw: expected CUDA tensors of one type, bf16 or f16")
+    rows, k, x_ld = _rows(x, index, "x")
+    dy_rows, n, dy_ld = _rows(dy, index, "dy")
+    if dy_rows != rows:
+        _refuse(f"dy, x: {dy_rows} and {rows} rows")
     groups = 1 if offsets is None else offsets.numel() - 1
     off = _offsets(offsets, groups, index)
-    dy_ld = _row_stride(dy, rows, n, "dy", index)
-    x_ld = _row_stride(x, rows, k, "x", index)
-    out, o, o_ld = _output(out, (n, k) if offsets is None else (groups, n, k),
-                           torch.float32 if out_dtype is None and out is None else out_dtype, accumulate, index, stream)
+    if out is None and out_dtype is None:
+        out_dtype = torch.float32
+    out, o, o_ld = _output(out, (n, k) if offsets is None else (groups, n, k), out_dtype, accumulate, index, stream)
     io = _pack_gemm(groups, rows, n, k, t, o, 1 if accumulate else 0, off, x.data_ptr(), x_ld, 0, dy.data_ptr(), dy_ld, 0, 0, 0,
                     out.data_ptr(), o_ld)
     _enqueue(lib().nvfp4_moe_grouped_gemm_dw, io, index, stream, "nvfp4_moe_grouped_gemm_dw")
