@@ -18,8 +18,9 @@
 // A CTA, or a pair of CTAs as one cta_group::2 (then M = 256, each CTA holding 128 rows
 // of A and half of B's columns: half the shared-memory traffic per MMA), walks its tiles
 // in a fixed stride over all groups' tiles, which every CTA lists for itself from the
-// offsets at its start: no host read-back, no workspace, no second launch. The sums'
-// order does not depend on timing.
+// offsets at its start: no host read-back, no workspace, no second launch. Where a few
+// tiles have long sums, the CTAs of a cluster take a part of each and join them through
+// each other's shared memory. The sums' order does not depend on timing.
 #include <algorithm>
 #include <cstring>
 #include <mutex>
@@ -54,6 +55,7 @@ struct MmaParams {
     int32_t bn, bn_log2;   // most rows of a tile (N): 64, 128 or 256
     int32_t box;           // rows of the larger K-major B box
     int32_t stages;
+    int32_t split;         // one-CTA tiles: CTAs of a cluster that share a tile's sum (1: none)
     int32_t staged;        // whole batches of outputs leave as boxes (map_o is set); rows are 16-byte aligned
     int32_t a_whole, b_whole;   // M- or N-major operands: all of a stage's 64-column boxes as one
 };
@@ -79,7 +81,7 @@ struct __align__(16) OutTile {
     int32_t m0;      // first output column
     int32_t row0;    // first output row: of all rows (product, dx), of the group's matrix (dw)
     int32_t nrow;    // output rows of the tile (1..bn)
-    int32_t c0, c;   // the summed index: first and count (dw: the group's rows)
+    int32_t c0, c;   // the summed index: first and count (dw: among all rows), of this CTA's part
     int32_t pad[2];
 };
 
@@ -334,7 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
-    const int cid = (int)blockIdx.x / CG, ncl = (int)gridDim.x / CG;
+    const bool split = CG == 1 && q.split > 1;
+    const int part = split ? (int)cluster_ctarank() : 0;   // of a tile's sum
+    const int share = CG == 1 ? q.split : CG, cid = (int)blockIdx.x / share, ncl = (int)gridDim.x / share;
     const int S = q.stages;
     constexpr int kStep = kI8 ? 128 : 64;   // the summed index's extent of a stage
 
@@ -453,6 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return t;
     };
+    OutTile mine;        // split sums: the epilogue warps' tile and its accumulator
+    int mine_buf = -1;
+    mine.e = -1;
     int stage = 0;
     uint32_t phase = 0;
     auto next = [&]() {
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (CG == 2) mbar_arrive(bar);   // the other CTA's arrival, which would take its time
                     }
                     if (MODE == kFwd)
-                        tma_3d<CG>(a, &map_a, bar, leader, c, acol, z);
+                        tma_3d<CG>(a, &map_a, bar, leader, c0 + c, acol, z);
                     else if (q.a_whole)
                         tma_4d<CG>(a, &map_a, bar, leader, acol / 64, c0 + c, z);
                     else
@@ -511,8 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else if (MODE == kDw)
                         for (int j = 0; j < nbox; j++) tma_3d<CG>(b + j * 64 * kLine, mb, bar, leader, brow + 64 * j, c0 + c, 0);
                     else {
-                        tma_3d<CG>(b, mb, bar, leader, c, brow, 0);
-                        if (nbox > 1) tma_3d<CG>(b + box * kLine, mb, bar, leader, c, brow + box, 0);
+                        tma_3d<CG>(b, mb, bar, leader, c0 + c, brow, 0);
+                        if (nbox > 1) tma_3d<CG>(b + box * kLine, mb, bar, leader, c0 + c, brow + box, 0);
                     }
                 }
                 __syncwarp();
@@ -539,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int e = uni(t.e), tc = uni(t.c);
                 const uint32_t idesc = q.idesc | (uint32_t)(uni(cdiv(t.nrow, 16 * CG)) * 2 * CG) << 17;
                 if (e < 0) break;
-                if (MODE == kDw && tc == 0) continue;
+                if (tc == 0) continue;
                 const int buf = it++ & 1;
                 const uint32_t d = d0 + buf * kAccCols;
                 ok = warp_wait<CG == 2>(&bars->acc_empty[buf], ((acc_phase >> buf) & 1) ^ 1, abort, 2);
@@ -615,6 +622,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             t.e = -1;
             const int i = round * ncl + (MODE == kDw && (round & 1) ? ncl - 1 - cid : cid);
             if (i < tiles.total) t = tiles.at(i);
+            if (split && t.e >= 0) {
+                const int steps = cdiv(t.c, kStep), per = cdiv(steps, q.split), from = min(part * per, steps) * kStep;
+                t.c0 += from;
+                t.c = max(0, min(t.c - from, per * kStep));
+            }
             if (!warp_wait<false>(&bars->tile_empty[slot], slot_phase ^ 1, abort, 8)) break;
             if (lane == 0) {
                 groups->ahead[slot] = t;
@@ -641,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *os = out_stage + half * kOutBytes;
         while (true) {
             const OutTile t = next_tile();
-            const bool none = MODE == kDw && t.e >= 0 && t.c == 0;   // an expert without rows: zeros
+            const bool none = t.e >= 0 && t.c == 0;   // an expert without rows (or a part of a short sum): zeros
             const int col0 = t.m0 + rank * 128, col = col0 + 32 * quarter + lane;   // of the CTA, of this lane
             const int64_t orow = (MODE == kDw ? (int64_t)t.e * q.p.n : 0) + t.row0;
             // Scales of int8 products come in while the sums are still being formed: of the
@@ -662,11 +674,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool go = t.e >= 0;
             if (go && !none) go = mbar_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, g_status, 5);
             if (!half_all(half, go)) break;
-            if (none && q.p.out_add) continue;
+            if (none && q.p.out_add && !split) continue;
             if (!none) {
                 it++;
                 acc_phase ^= 1u << buf;
                 tc_fence_after();
+            }
+            if (split) {   // its only tile: joined below
+                mine = t;
+                mine_buf = none ? -1 : buf;
+                break;
             }
             // this warp has read what it needs of the accumulator
             auto release = [&]() {
@@ -785,6 +802,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (storer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
+    if (split) {
+        // Every CTA leaves its sums in its own shared memory (its copies have all been
+        // consumed), [row][128 columns] of 32 bits; then each adds up an equal share of the
+        // rows, the parts in order, and writes it.
+        const int quarter = warp & 3, half = warp >> 2;
+        const bool some = warp < kEpiWarps && mine.e >= 0;
+        uint32_t *sums = reinterpret_cast<uint32_t *>(smem) + 32 * quarter + lane;
+        if (some)
+            for (int r = 32 * half; r < mine.nrow; r += 64) {
+                uint32_t u[32];
+                __syncwarp();
+                if (mine_buf >= 0) {
+                    tmem_ld32(tmem_base + mine_buf * kAccCols + ((uint32_t)(quarter * 32) << 16) + r, u);
+                    tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j++) u[j] = 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j++) sums[(r + j) * 128] = u[j];
+            }
+        __syncwarp();
+        cluster_sync_all();
+        const int cols = MODE == kFwd ? q.p.n : q.p.k, col = mine.m0 + 32 * quarter + lane;
+        if (some && col < cols) {
+            const int rows = cdiv(mine.nrow, q.split), end = min(mine.nrow, (part + 1) * rows);
+            const float cs = kI8 ? q.p.w_scale[(int64_t)mine.e * q.p.n + col] : 1.0f;
+            for (int r = part * rows + half; r < end; r += 8) {
+                uint32_t w[4][8];   // four rows (every second one), all parts
+#pragma unroll
+                for (int o = 0; o < 8; o++) {
+                    if (o >= q.split) break;
+                    const uint32_t from = mapa_shared(sums + r * 128, o);
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (r + 2 * j < end)
+                            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(w[j][o]) : "r"(from + j * 1024) : "memory");
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int row = r + 2 * j;
+                    if (row >= end) break;
+                    uint32_t u = w[j][0];
+#pragma unroll
+                    for (int o = 1; o < 8; o++)
+                        if (o < q.split) u = kI8 ? u + w[j][o] : __float_as_uint(__uint_as_float(u) + __uint_as_float(w[j][o]));
+                    float v = __uint_as_float(u);
+                    if (kI8) v = (float)(int32_t)u * (q.p.x_scale[mine.row0 + row] * cs);
+                    const int64_t at = ((MODE == kDw ? (int64_t)mine.e * q.p.n : 0) + mine.row0 + row) * q.p.out_ld + col;
+                    if constexpr (kF32) {
+                        float *out = static_cast<float *>(q.p.out) + at;
+                        *out = q.p.out_add ? *out + v : v;
+                    } else if (q.out_type == NVFP4_MOE_TYPE_BF16)
+                        static_cast<__nv_bfloat16 *>(q.p.out)[at] = __float2bfloat16_rn(v);
+                    else
+                        static_cast<__half *>(q.p.out)[at] = __float2half_rn(v);
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();   // the sums have been read
+    }
+
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -866,17 +946,17 @@ MmaKernel kernel_of(int mode, bool i8, int cg, bool f32) {
                    : (f32 ? kernel_of<2, true>(mode, i8) : kernel_of<2, false>(mode, i8));
 }
 
-cudaLaunchConfig_t config(int grid, int cg, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr) {
+cudaLaunchConfig_t config(int grid, int cluster, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = cg;
+    attr->val.clusterDim.x = cluster;
     attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cg > 1 ? 1 : 0;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
     return cfg;
 }
 
@@ -884,6 +964,7 @@ cudaLaunchConfig_t config(int grid, int cg, size_t smem, cudaStream_t s, cudaLau
 struct Resident {
     bool done;
     int ctas, pairs;
+    int split[9];   // clusters of 2, 4 and 8 one-CTA tiles
 };
 std::mutex g_mu;
 Resident g_resident[64];
@@ -908,16 +989,27 @@ cudaError_t resident(Resident *out) {
         e = cudaOccupancyMaxActiveClusters(&r.pairs, kernel_of(kFwd, false, 2, false), &cfg);
         if (e != cudaSuccess) return e;
         if (r.pairs < 1) return cudaErrorInvalidConfiguration;
+        for (int n = 2; n <= 8; n *= 2) {
+            const cudaLaunchConfig_t c = config(n, n, kSmemLimit, 0, &attr);
+            e = cudaOccupancyMaxActiveClusters(&r.split[n], kernel_of(kFwd, false, 1, false), &c);
+            if (e != cudaSuccess) return e;
+        }
         r.done = true;
     }
     *out = r;
     return cudaSuccess;
 }
 
-// The tile shape: CTAs to a tile and its most rows.
+// The tile shape: CTAs to a tile, its most rows, and CTAs that share its sum.
 struct Shape {
-    int cg, bn;
+    int cg, bn, split;
 };
+
+// The most tiles that there can be.
+int64_t most_tiles(int mode, const Product &p, int cols, const Shape &s) {
+    return (int64_t)cdiv(cols, 128 * s.cg) *
+           (mode == kDw ? (int64_t)p.groups * cdiv(p.n, s.bn) : (int64_t)p.rows / s.bn + std::min(p.groups, p.rows));
+}
 
 // By an estimate of the time, in cycles of a CTA (or pair), for groups of average size:
 // waves of tiles, each as long as the longer of its sum and its epilogue. A stage of a tile
@@ -926,20 +1018,25 @@ struct Shape {
 // besides, a pair 2000 once. Small tiles fill the GPU where there are few rows (201 rows x
 // 2048 x 768 int8: 6.4 us in tiles of 64, 9.7 in pairs of 256), pairs of 256 move the fewest
 // bytes an MMA (4096 x 2560 x 2560 BF16: 44 us, 69 in tiles of 64; 64 experts, 16384 pairs,
-// dx: 121 us, 131 in tiles of 64).
+// dx: 121 us, 131 in tiles of 64). Few tiles of long sums are split over clusters, whose
+// join costs about 3000 cycles (dw of one group, 10000 rows, 200 x 304: 43 us whole, 12 in eight
+// parts; 16384 rows, 512 x 512: 65 and 22 in four; 128 rows, 256 x 256: 6.0 and 6.9).
 Shape choose(int mode, const Product &p, bool i8, int cols, const Resident &r) {
-    static const Shape shapes[] = {{1, 64}, {1, 128}, {2, 128}, {2, 256}};
+    static const Shape shapes[] = {{1, 64, 1},  {1, 128, 1}, {2, 128, 1}, {2, 256, 1}, {1, 64, 2},
+                                   {1, 128, 2}, {1, 64, 4},  {1, 128, 4}, {1, 64, 8},  {1, 128, 8}};
     const int active = std::min(p.groups, p.rows), avg = cdiv(p.rows, active), step = i8 ? 128 : 64;
     Shape best = shapes[0];
     int64_t least = INT64_MAX;
     for (const Shape &s : shapes) {
+        if (s.split > 1 && most_tiles(mode, p, cols, s) > r.split[s.split]) continue;   // one tile to a cluster
         const int total = mode == kDw ? p.n : avg, nt = cdiv(total, s.bn), n = cdiv(total, nt);
         const int64_t tiles = (int64_t)cdiv(cols, 128 * s.cg) * nt * active;
-        const int stages = cdiv(mode == kFwd ? p.k : mode == kDx ? p.n : avg, step);
+        const int stages = cdiv(cdiv(mode == kFwd ? p.k : mode == kDx ? p.n : avg, step), s.split);
         const int64_t sum = (int64_t)stages * (s.cg == 1 ? std::max(380, n * 37 / 10) : std::max(400, n * 11 / 4));
-        const int64_t units = s.cg == 1 ? r.ctas : r.pairs;
-        const int64_t cost = (tiles + units - 1) / units * (std::max<int64_t>(sum, n * 13) + 1200) + (s.cg == 2 ? 2000 : 0);
-        if (cost <= least) {   // of equals the larger: groups are seldom all of a size
+        const int64_t units = s.split > 1 ? r.split[s.split] : s.cg == 1 ? r.ctas : r.pairs;
+        const int64_t cost = (tiles + units - 1) / units * (std::max<int64_t>(sum, n * 13) + 1200) + (s.cg == 2 ? 2000 : 0) +
+                             (s.split > 1 ? 3000 : 0);
+        if (s.split > 1 ? cost < least : cost <= least) {   // of equals the larger: groups are seldom all of a size
             least = cost;
             best = s;
         }
@@ -988,13 +1085,13 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     if (ok && mode != kDw) ok = map_operand(&b_small, ob, type, kBoxSmall, 0);
     if (ok && q.staged) ok = map_output(&o, p.out, out, out_rows, cols, p.out_ld);
     if (!ok) return cudaErrorInvalidValue;
+    q.split = shape.split;
     // no more CTAs than there can be tiles
-    const int64_t mt = cdiv(cols, 128 * cg);
-    const int64_t most = mt * (mode == kDw ? (int64_t)p.groups * cdiv(p.n, q.bn)
-                                           : (int64_t)p.rows / q.bn + std::min(p.groups, p.rows));
-    const int units = (int)std::min<int64_t>(cg == 2 ? r.pairs : r.ctas, std::max<int64_t>(most, 1));
+    const int64_t most = std::max<int64_t>(most_tiles(mode, p, cols, shape), 1);
+    const int units = (int)std::min<int64_t>(q.split > 1 ? r.split[q.split] : cg == 2 ? r.pairs : r.ctas, most);
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = config(units * cg, cg, smem_bytes(q.bn, cg, q.stages), s, &attr);
+    const int cluster = cg * q.split;
+    const cudaLaunchConfig_t cfg = config(units * cluster, cluster, smem_bytes(q.bn, cg, q.stages), s, &attr);
     return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg, out == NVFP4_MOE_TYPE_F32), q, a, b, b_small, o);
 }
 

@@ -503,6 +503,44 @@ def test_large_tiles(counts, n, k, dtype, wide):
                nv.grouped_gemm_dw(dy, x, off, out_dtype=wide), wide)
 
 
+@pytest.mark.parametrize("counts,n,k", [
+    ((10000,), 200, 304), ((3001,), 130, 72), ((2000, 0, 71, 900), 96, 136), ((16384,), 64, 64), ((700,), 520, 40),
+    ((5, 4000), 33, 129), ((300,), 256, 4104), ((300,), 4104, 256),
+])
+def test_long_sums_of_few_tiles(counts, n, k):
+    """Sums that several CTAs share: the three products, accumulated ones too."""
+    off, rows, E = offsets_of(counts), sum(counts), len(counts)
+    x, dy, w = normal((rows, k), BF16, 145), normal((rows, n), BF16, 146, 0.5), normal((E, n, k), BF16, 147, 0.1)
+    for wide in (BF16, F32):
+        _check_all(x, dy, w, off.tolist(), nv.grouped_gemm(x, w, off, out_dtype=wide),
+                   nv.grouped_gemm_dx(dy, w, off, out_dtype=wide), nv.grouped_gemm_dw(dy, x, off, out_dtype=wide), wide)
+    base = torch.randn(E, n, k, generator=gen(148), device=DEV)
+    out = base.clone()
+    nv.grouped_gemm_dw(dy, x, off, out=out, accumulate=True)
+    assert (out == base + nv.grouped_gemm_dw(dy, x, off)).all()
+    for _ in range(3):
+        assert torch.equal(nv.grouped_gemm_dw(dy, x, off), nv.grouped_gemm_dw(dy, x, off))
+
+
+@pytest.mark.parametrize("rows,n,k", [(600, 256, 8208), (257, 40, 16384), (70, 130, 4000)])
+def test_int8_long_sums(rows, n, k):
+    x, w = codes((rows, k), 175), codes((n, k), 176)
+    xs, ws = torch.rand(rows, generator=gen(177), device=DEV) + 0.5, torch.rand(n, generator=gen(178), device=DEV) + 0.5
+    ref = (x.double() @ w.double().T) * xs[:, None].double() * ws.double()
+    for out_dtype in (F32, BF16):
+        got = nv.gemm_int8(x, w, xs, ws, out_dtype=out_dtype)
+        assert_within(got, ref, 4 * 2.0 ** -24 * ref.abs() + (half_step(out_dtype, ref) * (1 + 2.0 ** -8) if out_dtype != F32 else 0), "int8")
+
+
+def test_no_rows():
+    w = normal((3, 40, 64), BF16, 179)
+    off = torch.zeros(4, dtype=torch.int32, device=DEV)
+    assert nv.grouped_gemm(torch.empty(0, 64, dtype=BF16, device=DEV), w, off).shape == (0, 40)
+    assert nv.grouped_gemm_dx(torch.empty(0, 40, dtype=BF16, device=DEV), w, off).shape == (0, 64)
+    q, scale = nv.quantize_int8(torch.empty(0, 64, dtype=BF16, device=DEV))
+    assert q.shape == (0, 64) and scale.shape == (0,)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_outputs_with_rows_of_any_alignment(dtype):
     """Outputs whose rows start anywhere, with what lies between and around them left alone."""
