@@ -107,20 +107,38 @@ __device__ inline void load8(const T *p, int c, int cols, uint32_t (&w)[sizeof(T
     }
 }
 
+// Loads a chunk; with 16-bit gate | up their eight words stand where form_chunk leaves h, so
+// that all of a thread's loads are under way before the first of them is needed.
 template <typename T, bool kSwiglu, bool kVec>
 __device__ inline void load_chunk(Chunk<T, kSwiglu> &k, const T *in, int c, int cols) {
     if constexpr (!kSwiglu)
         load8<T, kVec>(in, c, cols, k.w);
-    else {
-        Chunk<T, false> g, u;
-        load8<T, kVec>(in, c, cols, g.w);
-        load8<T, kVec>(in + cols, c, cols, u.w);
+    else if constexpr (sizeof(T) == 2) {
+        uint32_t g[4], u[4];
+        load8<T, kVec>(in, c, cols, g);
+        load8<T, kVec>(in + cols, c, cols, u);
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const float2 a = g.pair(i), b = u.pair(i);
-            k.w[2 * i] = __float_as_uint(silu(a.x) * b.x);
-            k.w[2 * i + 1] = __float_as_uint(silu(a.y) * b.y);
+            k.w[i] = g[i];
+            k.w[4 + i] = u[i];
         }
+    } else {
+        uint32_t g[8], u[8];
+        load8<T, kVec>(in, c, cols, g);
+        load8<T, kVec>(in + cols, c, cols, u);
+#pragma unroll
+        for (int i = 0; i < 8; i++) k.w[i] = __float_as_uint(silu(__uint_as_float(g[i])) * __uint_as_float(u[i]));
+    }
+}
+template <typename T, bool kSwiglu>
+__device__ inline void form_chunk(Chunk<T, kSwiglu> &k) {
+    if constexpr (kSwiglu && sizeof(T) == 2) {
+        uint32_t r[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) r[i] = k.w[i];
+        const T *g = reinterpret_cast<const T *>(r), *u = reinterpret_cast<const T *>(r + 4);
+#pragma unroll
+        for (int i = 0; i < 8; i++) k.w[i] = __float_as_uint(silu(to_f32(g[i])) * to_f32(u[i]));
     }
 }
 
@@ -186,10 +204,14 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const nvfp4_moe_quan
             if (8 * (kPer * i + me) < cols) load_chunk<T, kSwiglu, kVec>(v[i], in, 8 * (kPer * i + me), cols);
 #pragma unroll
         for (int i = 0; i < kKeep; i++)
-            if (8 * (kPer * i + me) < cols) m = v[i].top(m);
+            if (8 * (kPer * i + me) < cols) {
+                form_chunk(v[i]);
+                m = v[i].top(m);
+            }
     } else {
         for (int c = 8 * me; c < cols; c += 8 * kPer) {
             load_chunk<T, kSwiglu, kVec>(v[0], in, c, cols);
+            form_chunk(v[0]);
             m = v[0].top(m);
         }
     }
@@ -212,6 +234,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const nvfp4_moe_quan
     } else {
         for (int c = 8 * me; c < cols; c += 8 * kPer) {
             load_chunk<T, kSwiglu, kVec>(v[0], in, c, cols);
+            form_chunk(v[0]);
             code_chunk<T, kSwiglu, kVec>(v[0], scale, inv, q, c, cols);
         }
     }
