@@ -85,17 +85,27 @@ struct __align__(16) OutTile {
     int32_t pad[2];
 };
 
-// The groups' rows, and the number of row tiles before each; the tiles listed ahead.
+// Shared memory behind the barriers: the tiles listed ahead, the groups' rows and the number
+// of row tiles before each. As long as there are groups, for every KB counts: with up to
+// about 180 of them (dw: 128) a sixth stage of a pair's tiles fits.
 struct Groups {
-    OutTile ahead[kTilesAhead];
-    int32_t lo[NVFP4_MOE_MAX_GROUPS + 1];   // first row, and the last group's end
-    int32_t before[NVFP4_MOE_MAX_GROUPS + 1];   // (dw: the groups by falling rows)
-    int32_t warp_sum[kThreads / 32], warp_max[kThreads / 32];
+    OutTile *ahead;                    // [kTilesAhead]
+    int32_t *warp_sum, *warp_max;      // [kThreads / 32]
+    int32_t *lo;                       // [groups + 1]: first row, and the last group's end
+    int32_t *before;                   // [groups + 1]; dw: the groups by falling rows [the next power of two]
+    __device__ Groups(void *p, int groups)
+        : ahead(static_cast<OutTile *>(p)), warp_sum(reinterpret_cast<int32_t *>(ahead + kTilesAhead)),
+          warp_max(warp_sum + kThreads / 32), lo(warp_max + kThreads / 32), before(lo + groups + 1) {}
 };
+inline size_t groups_bytes(int groups) {
+    int all = 1;
+    while (all < groups) all *= 2;
+    return kTilesAhead * sizeof(OutTile) + 4 * (2 * kThreads / 32 + (groups + 1) + std::max(groups + 1, all));
+}
 
 inline size_t stage_bytes(int bn, int cg) { return kABytes + (size_t)bn / cg * kLine; }
-inline size_t smem_bytes(int bn, int cg, int stages) {
-    return 1024 + stages * stage_bytes(bn, cg) + 2 * kOutBytes + sizeof(Bars) + sizeof(Groups);
+inline size_t smem_bytes(int bn, int cg, int stages, int groups) {
+    return 1024 + stages * stage_bytes(bn, cg) + 2 * kOutBytes + sizeof(Bars) + groups_bytes(groups);
 }
 
 template <int CG>
@@ -321,7 +331,7 @@ struct Tiles {
     }
 };
 
-template <int MODE, bool kI8, int CG, bool kF32>
+template <int MODE, bool kI8, int CG, bool kF32, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     product_mma_kernel(const __grid_constant__ MmaParams q, const __grid_constant__ CUtensorMap map_a,
                        const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_b_small,
@@ -331,14 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t b_bytes = (uint32_t)q.bn / CG * kLine, stage_size = kABytes + b_bytes;
     uint8_t *out_stage = smem + q.stages * stage_size;
     Bars *bars = reinterpret_cast<Bars *>(out_stage + 2 * kOutBytes);
-    Groups *groups = reinterpret_cast<Groups *>(bars + 1);
+    const Groups groups(bars + 1, q.p.groups);
     volatile int *abort = &bars->abort;
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 1 ? 0 : (int)cluster_ctarank();
-    const bool split = CG == 1 && q.split > 1;
-    const int part = split ? (int)cluster_ctarank() : 0;   // of a tile's sum
-    const int share = CG == 1 ? q.split : CG, cid = (int)blockIdx.x / share, ncl = (int)gridDim.x / share;
+    const int part = kSplit ? (int)cluster_ctarank() : 0;   // of a tile's sum
+    const int share = kSplit ? q.split : CG, cid = (int)blockIdx.x / share, ncl = (int)gridDim.x / share;
     const int S = q.stages;
     constexpr int kStep = kI8 ? 128 : 64;   // the summed index's extent of a stage
 
@@ -368,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!q.p.offsets) {   // one group of all rows
         if (threadIdx.x == 0) {
-            groups->lo[0] = groups->before[0] = 0;
-            groups->lo[1] = q.p.rows;
-            groups->before[1] = (q.p.rows + q.bn - 1) >> q.bn_log2;
+            groups.lo[0] = groups.before[0] = 0;
+            groups.lo[1] = q.p.rows;
+            groups.before[1] = (q.p.rows + q.bn - 1) >> q.bn_log2;
         }
     } else {
         // The groups' rows and row tiles, four groups a thread: offsets clamped into the
@@ -385,17 +394,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) top = max(top, __shfl_up_sync(0xffffffffu, top, d));   // (itself below d)
-        if (lane == 31) groups->warp_max[warp] = top;
+        if (lane == 31) groups.warp_max[warp] = top;
         __syncthreads();
         int run = __shfl_up_sync(0xffffffffu, top, 1);
         if (lane == 0) run = 0;
-        run = max(run, __reduce_max_sync(0xffffffffu, lane < warp ? groups->warp_max[lane] : 0));
+        run = max(run, __reduce_max_sync(0xffffffffu, lane < warp ? groups.warp_max[lane] : 0));
         int tiles[kPer], sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
             run = max(run, off[i]);
             const int count = max(off[i + 1] - run, 0);
-            if (e0 + i <= E) groups->lo[e0 + i] = run;
+            if (e0 + i <= E) groups.lo[e0 + i] = run;
             tiles[i] = e0 + i < E ? (count + q.bn - 1) >> q.bn_log2 : 0;
             sum += tiles[i];
         }
@@ -405,12 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int o = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += o;
         }
-        if (lane == 31) groups->warp_sum[warp] = upto;
+        if (lane == 31) groups.warp_sum[warp] = upto;
         __syncthreads();
-        upto += __reduce_add_sync(0xffffffffu, lane < warp ? groups->warp_sum[lane] : 0) - sum;
+        upto += __reduce_add_sync(0xffffffffu, lane < warp ? groups.warp_sum[lane] : 0) - sum;
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
-            if (MODE != kDw && e0 + i <= E) groups->before[e0 + i] = upto;
+            if (MODE != kDw && e0 + i <= E) groups.before[e0 + i] = upto;
             upto += tiles[i];
         }
         if (MODE == kDw) {
@@ -419,9 +428,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // of uneven popularity took 139 us in their own order and 109 us evenly filled.
             int all = 1;
             while (all < E) all *= 2;
-            uint32_t *key = reinterpret_cast<uint32_t *>(groups->before);
+            uint32_t *key = reinterpret_cast<uint32_t *>(groups.before);
             for (int e = threadIdx.x; e < all; e += kThreads)
-                key[e] = e < E ? (uint32_t)min(groups->lo[e + 1] - groups->lo[e], (1 << 21) - 1) << 10 | e : 0u;
+                key[e] = e < E ? (uint32_t)min(groups.lo[e + 1] - groups.lo[e], (1 << 21) - 1) << 10 | e : 0u;
             for (int size = 2; size <= all; size *= 2)
                 for (int d = size / 2; d > 0; d /= 2) {
                     __syncthreads();
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         OutTile t;
         t.e = -1;
         if (warp_wait<false>(&bars->tile_full[slot], slot_phase, abort, 7)) {
-            t = groups->ahead[slot];
+            t = groups.ahead[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->tile_empty[slot]);
             if (++slot == kTilesAhead) { slot = 0; slot_phase ^= 1; }
@@ -546,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int e = uni(t.e), tc = uni(t.c);
                 const uint32_t idesc = q.idesc | (uint32_t)(uni(cdiv(t.nrow, 16 * CG)) * 2 * CG) << 17;
                 if (e < 0) break;
-                if (tc == 0) continue;
+                if ((MODE == kDw || kSplit) && tc == 0) continue;
                 const int buf = it++ & 1;
                 const uint32_t d = d0 + buf * kAccCols;
                 ok = warp_wait<CG == 2>(&bars->acc_empty[buf], ((acc_phase >> buf) & 1) ^ 1, abort, 2);
@@ -616,20 +625,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kTileWarp) {
         // ---------------------------------------------------- lists the tiles
-        const Tiles<MODE, CG> tiles(q, *groups);
+        const Tiles<MODE, CG> tiles(q, groups);
         for (int round = 0; ; round++) {
             OutTile t;
             t.e = -1;
             const int i = round * ncl + (MODE == kDw && (round & 1) ? ncl - 1 - cid : cid);
             if (i < tiles.total) t = tiles.at(i);
-            if (split && t.e >= 0) {
+            if (kSplit && t.e >= 0) {
                 const int steps = cdiv(t.c, kStep), per = cdiv(steps, q.split), from = min(part * per, steps) * kStep;
                 t.c0 += from;
                 t.c = max(0, min(t.c - from, per * kStep));
             }
             if (!warp_wait<false>(&bars->tile_empty[slot], slot_phase ^ 1, abort, 8)) break;
             if (lane == 0) {
-                groups->ahead[slot] = t;
+                groups.ahead[slot] = t;
                 mbar_arrive(&bars->tile_full[slot]);
             }
             __syncwarp();
@@ -653,7 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *os = out_stage + half * kOutBytes;
         while (true) {
             const OutTile t = next_tile();
-            const bool none = t.e >= 0 && t.c == 0;   // an expert without rows (or a part of a short sum): zeros
+            // zeros: an expert without rows, or a part of a short sum
+            const bool none = (MODE == kDw || kSplit) && t.e >= 0 && t.c == 0;
             const int col0 = t.m0 + rank * 128, col = col0 + 32 * quarter + lane;   // of the CTA, of this lane
             const int64_t orow = (MODE == kDw ? (int64_t)t.e * q.p.n : 0) + t.row0;
             // Scales of int8 products come in while the sums are still being formed: of the
@@ -674,13 +684,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool go = t.e >= 0;
             if (go && !none) go = mbar_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, g_status, 5);
             if (!half_all(half, go)) break;
-            if (none && q.p.out_add && !split) continue;
+            if (none && q.p.out_add && !kSplit) continue;
             if (!none) {
                 it++;
                 acc_phase ^= 1u << buf;
                 tc_fence_after();
             }
-            if (split) {   // its only tile: joined below
+            if (kSplit) {   // its only tile: joined below
                 mine = t;
                 mine_buf = none ? -1 : buf;
                 break;
@@ -802,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (storer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
-    if (split) {
+    if constexpr (kSplit) {
         // Every CTA leaves its sums in its own shared memory (its copies have all been
         // consumed), [row][128 columns] of 32 bits; then each adds up an equal share of the
         // rows, the parts in order, and writes it.
@@ -934,16 +944,17 @@ bool map_output(CUtensorMap *m, void *base, nvfp4_moe_type type, int64_t rows, i
 
 typedef void (*MmaKernel)(const MmaParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap);
 
-template <int CG, bool kF32>
+template <int CG, bool kF32, bool kSplit>
 MmaKernel kernel_of(int mode, bool i8) {
-    if (i8) return product_mma_kernel<kFwd, true, CG, kF32>;
-    return mode == kFwd ? product_mma_kernel<kFwd, false, CG, kF32>
-           : mode == kDx ? product_mma_kernel<kDx, false, CG, kF32>
-                         : product_mma_kernel<kDw, false, CG, kF32>;
+    if (i8) return product_mma_kernel<kFwd, true, CG, kF32, kSplit>;
+    return mode == kFwd  ? product_mma_kernel<kFwd, false, CG, kF32, kSplit>
+           : mode == kDx ? product_mma_kernel<kDx, false, CG, kF32, kSplit>
+                         : product_mma_kernel<kDw, false, CG, kF32, kSplit>;
 }
-MmaKernel kernel_of(int mode, bool i8, int cg, bool f32) {
-    return cg == 1 ? (f32 ? kernel_of<1, true>(mode, i8) : kernel_of<1, false>(mode, i8))
-                   : (f32 ? kernel_of<2, true>(mode, i8) : kernel_of<2, false>(mode, i8));
+MmaKernel kernel_of(int mode, bool i8, int cg, bool f32, bool split) {
+    if (cg == 2) return f32 ? kernel_of<2, true, false>(mode, i8) : kernel_of<2, false, false>(mode, i8);
+    if (split) return f32 ? kernel_of<1, true, true>(mode, i8) : kernel_of<1, false, true>(mode, i8);
+    return f32 ? kernel_of<1, true, false>(mode, i8) : kernel_of<1, false, false>(mode, i8);
 }
 
 cudaLaunchConfig_t config(int grid, int cluster, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr) {
@@ -977,8 +988,9 @@ cudaError_t resident(Resident *out) {
     std::lock_guard<std::mutex> lock(g_mu);
     Resident &r = g_resident[dev];
     if (!r.done) {
-        for (int i = 0; i < 16; i++) {
-            e = cudaFuncSetAttribute(kernel_of(i % 4 % 3, i % 4 == 3, 1 + (i >> 2 & 1), i >> 3),
+        for (int i = 0; i < 24; i++) {   // product, dx, dw and int8; one CTA, a pair, a split sum; 16 bits and 32
+            const int kind = i % 4, form = i / 4 % 3;
+            e = cudaFuncSetAttribute(kernel_of(kind % 3, kind == 3, form == 1 ? 2 : 1, i >= 12, form == 2),
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
             if (e != cudaSuccess) return e;
         }
@@ -986,12 +998,12 @@ cudaError_t resident(Resident *out) {
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute attr;
         const cudaLaunchConfig_t cfg = config(2, 2, kSmemLimit, 0, &attr);
-        e = cudaOccupancyMaxActiveClusters(&r.pairs, kernel_of(kFwd, false, 2, false), &cfg);
+        e = cudaOccupancyMaxActiveClusters(&r.pairs, kernel_of(kFwd, false, 2, false, false), &cfg);
         if (e != cudaSuccess) return e;
         if (r.pairs < 1) return cudaErrorInvalidConfiguration;
         for (int n = 2; n <= 8; n *= 2) {
             const cudaLaunchConfig_t c = config(n, n, kSmemLimit, 0, &attr);
-            e = cudaOccupancyMaxActiveClusters(&r.split[n], kernel_of(kFwd, false, 1, false), &c);
+            e = cudaOccupancyMaxActiveClusters(&r.split[n], kernel_of(kFwd, false, 1, false, true), &c);
             if (e != cudaSuccess) return e;
         }
         r.done = true;
@@ -1019,7 +1031,7 @@ int64_t most_tiles(int mode, const Product &p, int cols, const Shape &s) {
 // 2048 x 768 int8: 6.4 us in tiles of 64, 9.7 in pairs of 256), pairs of 256 move the fewest
 // bytes an MMA (4096 x 2560 x 2560 BF16: 44 us, 69 in tiles of 64; 64 experts, 16384 pairs,
 // dx: 121 us, 131 in tiles of 64). Few tiles of long sums are split over clusters, whose
-// join costs about 3000 cycles (dw of one group, 10000 rows, 200 x 304: 43 us whole, 12 in eight
+// join costs about 4500 cycles (dw of one group, 10000 rows, 200 x 304: 43 us whole, 12 in eight
 // parts; 16384 rows, 512 x 512: 65 and 22 in four; 128 rows, 256 x 256: 6.0 and 6.9).
 Shape choose(int mode, const Product &p, bool i8, int cols, const Resident &r) {
     static const Shape shapes[] = {{1, 64, 1},  {1, 128, 1}, {2, 128, 1}, {2, 256, 1}, {1, 64, 2},
@@ -1035,7 +1047,7 @@ Shape choose(int mode, const Product &p, bool i8, int cols, const Resident &r) {
         const int64_t sum = (int64_t)stages * (s.cg == 1 ? std::max(380, n * 37 / 10) : std::max(400, n * 11 / 4));
         const int64_t units = s.split > 1 ? r.split[s.split] : s.cg == 1 ? r.ctas : r.pairs;
         const int64_t cost = (tiles + units - 1) / units * (std::max<int64_t>(sum, n * 13) + 1200) + (s.cg == 2 ? 2000 : 0) +
-                             (s.split > 1 ? 3000 : 0);
+                             (s.split > 1 ? 4500 : 0);
         if (s.split > 1 ? cost < least : cost <= least) {   // of equals the larger: groups are seldom all of a size
             least = cost;
             best = s;
@@ -1065,7 +1077,7 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     q.bn = shape.bn;
     q.bn_log2 = q.bn == 64 ? 6 : q.bn == 128 ? 7 : 8;
     q.box = std::min(128, q.bn / cg);
-    q.stages = (int)std::min<size_t>(kMaxStages, (kSmemLimit - smem_bytes(q.bn, cg, 0)) / stage_bytes(q.bn, cg));
+    q.stages = (int)std::min<size_t>(kMaxStages, (kSmemLimit - smem_bytes(q.bn, cg, 0, p.groups)) / stage_bytes(q.bn, cg));
     // D F32 (or S32), A and B F16, BF16 or S8, their majors, M
     q.idesc = i8 ? (2u << 4) | (1u << 7) | (1u << 10) : (1u << 4) | (type == NVFP4_MOE_TYPE_BF16 ? (1u << 7) | (1u << 10) : 0u);
     if (mode != kFwd) q.idesc |= 1u << 15;
@@ -1091,8 +1103,8 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     const int units = (int)std::min<int64_t>(q.split > 1 ? r.split[q.split] : cg == 2 ? r.pairs : r.ctas, most);
     cudaLaunchAttribute attr;
     const int cluster = cg * q.split;
-    const cudaLaunchConfig_t cfg = config(units * cluster, cluster, smem_bytes(q.bn, cg, q.stages), s, &attr);
-    return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg, out == NVFP4_MOE_TYPE_F32), q, a, b, b_small, o);
+    const cudaLaunchConfig_t cfg = config(units * cluster, cluster, smem_bytes(q.bn, cg, q.stages, p.groups), s, &attr);
+    return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg, out == NVFP4_MOE_TYPE_F32, q.split > 1), q, a, b, b_small, o);
 }
 
 int product_status(cudaStream_t s) {
