@@ -76,7 +76,7 @@ def products_status(stream=None) -> int:
 # packed rather than built field by field, and messages are put together only where a check
 # fails.
 
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice         # torch.cuda.current_device() (a CUDA tensor is at hand: no set-up to do)
 _raw_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stream().cuda_stream, without its object
 _empty = torch.empty_strided   # half the time of torch.empty, and it pads rows without a view
 _UNIT = {torch.bfloat16: 8, torch.float16: 8, torch.float32: 4, torch.int8: 16}   # values in 16 bytes
@@ -104,7 +104,7 @@ def _rows(t, index: int, name: str):
     if rows > 1:
         return rows, cols, stride[0]
     unit = _UNIT[t.dtype]
-    return rows, cols, -(-cols // unit) * unit   # one row: no stride to take
+    return rows, cols, (cols + unit - 1) & -unit   # one row: no stride to take
 
 
 def _matrices(t, index: int, name: str):
@@ -129,7 +129,7 @@ def _matrices(t, index: int, name: str):
         _refuse(f"{name}: expected contiguous rows")
     if n <= 1 and groups <= 1:
         unit = _UNIT[t.dtype]
-        ld = -(-k // unit) * unit
+        ld = (k + unit - 1) & -unit
     return groups, n, k, ld
 
 
@@ -150,7 +150,12 @@ def _output(out, shape, dtype, accumulate: bool, index: int, stream):
         t = _TYPES.get(dtype, TYPE_INT8)
         if t == TYPE_INT8:
             _refuse("out_dtype: expected bf16, f16 or f32")
-        out, ld = _new(shape, dtype, index, stream)
+        if stream is not None or len(shape) == 3:
+            out, ld = _new(shape, dtype, index, stream)
+        else:
+            unit = _UNIT[dtype]
+            ld = (shape[1] + unit - 1) & -unit
+            out = _empty(shape, (ld, 1), dtype=dtype, device=index)
         return out, t, ld
     t = _TYPES.get(out.dtype, TYPE_INT8)
     if t == TYPE_INT8 or tuple(out.shape) != tuple(shape) or (dtype is not None and out.dtype != dtype):
@@ -163,10 +168,9 @@ def _new(shape, dtype, index: int, stream):
     if stream is not None:
         with torch.cuda.stream(stream):
             return _new(shape, dtype, index, None)
-    cols, unit = shape[-1], _UNIT[dtype]
-    ld = -(-cols // unit) * unit
-    strides = (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1)
-    return _empty(shape, strides, dtype=dtype, device=index), ld
+    unit = _UNIT[dtype]
+    ld = (shape[-1] + unit - 1) & -unit
+    return _empty(shape, (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1), dtype=dtype, device=index), ld
 
 
 def _enqueue(fn, io: bytes, index: int, stream, what: str) -> None:
@@ -221,6 +225,10 @@ def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, ou
     (or [n][k]), both bf16, f16, or int8 with x_scale [rows] and w_scale [groups][n] f32.
     out: [rows][n], by default of x's type (f32 for int8); rows of no group are not written.
     accumulate: out += (f32)."""
+    return _product(x, w, offsets, x_scale, w_scale, out, out_dtype, accumulate, stream)
+
+
+def _product(x, w, offsets, x_scale, w_scale, out, out_dtype, accumulate, stream):
     dtype, index = x.dtype, x.get_device()
     t = _TYPES.get(dtype, TYPE_F32)
     if index < 0 or t == TYPE_F32 or w.dtype is not dtype:
@@ -253,8 +261,7 @@ def gemm_int8(x, w, x_scale, w_scale, *, out=None, out_dtype=None, accumulate: b
     int8, w: [n][k] int8, scales f32. out: [rows][n], f32 by default. accumulate: out += (f32)."""
     if x.dtype is not torch.int8 or w.dim() != 2:
         _refuse("x, w: expected int8 [rows][k] and [n][k]")
-    return grouped_gemm(x, w, None, x_scale=x_scale, w_scale=w_scale, out=out, out_dtype=out_dtype,
-                        accumulate=accumulate, stream=stream)
+    return _product(x, w, None, x_scale, w_scale, out, out_dtype, accumulate, stream)
 
 
 def grouped_gemm_dx(dy, w, offsets=None, *, out=None, out_dtype=None, accumulate: bool = False, stream=None):
