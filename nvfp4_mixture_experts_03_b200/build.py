@@ -1,4 +1,5 @@
-"""Builds libnvfp4_moe.so in-tree with nvcc for sm_100a (cross-compiles without a GPU)."""
+"""Builds libnvfp4_moe.so in-tree with nvcc for sm_100a (cross-compiles without a GPU), and
+_marshal.so, the torch binding of the products' common calls, with the host compiler."""
 from __future__ import annotations
 
 import glob
@@ -11,6 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libnvfp4_moe.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
@@ -30,7 +32,29 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def build_marshal(force: bool = False) -> str:
+    """csrc/marshal.cpp against the torch and the Python that run this."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    src, header = os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "nvfp4_moe_products.h")
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) > max(map(os.path.getmtime, (src, header))):
+        return MARSHAL
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
+                *cpp_extension.include_paths()]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    subprocess.check_call([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[f"-I{i}" for i in includes],
+                           src, "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
+    build_marshal(force)
     if not force and not _stale():
         return LIB
     objdir = os.path.join(HERE, "_build")

@@ -84,6 +84,23 @@ _pack_gemm = struct.Struct("@7iPPqPPqPqPPq").pack     # GemmIO
 _pack_quantize = struct.Struct("@4iPqPqP").pack       # QuantizeIO
 
 
+try:      # csrc/marshal.cpp: the common calls, natively; without it they take the Python below
+    from . import _marshal
+except ImportError:
+    _marshal = None
+_native = None   # _marshal, once the library is loaded
+
+
+def _set_up():
+    global _native
+    if _marshal is not None:
+        L = lib()
+        _marshal.setup(*[C.cast(getattr(L, f), C.c_void_p).value
+                         for f in ("nvfp4_moe_grouped_gemm", "nvfp4_moe_grouped_gemm_dx", "nvfp4_moe_grouped_gemm_dw",
+                                   "nvfp4_moe_quantize_int8")])
+        _native = _marshal
+
+
 def _refuse(what: str):
     raise ValueError(what)
 
@@ -173,6 +190,10 @@ def _new(shape, dtype, index: int, stream):
     return _empty(shape, (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1), dtype=dtype, device=index), ld
 
 
+def _failed(rc: int, what: str):
+    raise NVFP4MoEError(rc, what)
+
+
 def _enqueue(fn, io: bytes, index: int, stream, what: str) -> None:
     s = _raw_stream(index) if stream is None else stream.cuda_stream
     if _current_device() == index:
@@ -181,7 +202,9 @@ def _enqueue(fn, io: bytes, index: int, stream, what: str) -> None:
         with torch.cuda.device(index):
             rc = fn(io, s)
     if rc != OK:
-        raise NVFP4MoEError(rc, what)
+        _failed(rc, what)
+    if _native is None:
+        _set_up()
 
 
 def quantize_int8(x, *, swiglu: bool = False, q=None, scale=None, stream=None):
@@ -189,6 +212,12 @@ def quantize_int8(x, *, swiglu: bool = False, q=None, scale=None, stream=None):
     nearest whole number (ties to even). x: [rows][cols] bf16, f16 or f32; with `swiglu`
     [rows][2*cols] holding gate | up, and v = SiLU(gate) * up.
     Returns (q int8 [rows][cols], scale f32 [rows])."""
+    if _native is not None and q is None and scale is None and stream is None:
+        r = _native.quantize(x, swiglu)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            _failed(r, "nvfp4_moe_quantize_int8")
     t, index = _TYPES.get(x.dtype, TYPE_INT8), x.get_device()
     if t == TYPE_INT8 or index < 0:
         _refuse("quantize_int8: expected a CUDA tensor [rows][cols], bf16, f16 or f32")
@@ -229,6 +258,10 @@ def grouped_gemm(x, w, offsets=None, *, x_scale=None, w_scale=None, out=None, ou
 
 
 def _product(x, w, offsets, x_scale, w_scale, out, out_dtype, accumulate, stream):
+    if _native is not None and out is None and stream is None and not accumulate:
+        r = _native.product(0, x, w, offsets, x_scale, w_scale, out_dtype)
+        if r is not None:
+            return r if type(r) is not int else _failed(r, "nvfp4_moe_grouped_gemm")
     dtype, index = x.dtype, x.get_device()
     t = _TYPES.get(dtype, TYPE_F32)
     if index < 0 or t == TYPE_F32 or w.dtype is not dtype:
@@ -267,6 +300,10 @@ def gemm_int8(x, w, x_scale, w_scale, *, out=None, out_dtype=None, accumulate: b
 def grouped_gemm_dx(dy, w, offsets=None, *, out=None, out_dtype=None, accumulate: bool = False, stream=None):
     """The gradient of grouped_gemm for x: dx[p] = dy[p] W_e. dy: [rows][n], w: [groups][n][k],
     both bf16 or f16. out: [rows][k], by default of dy's type; rows of no group are not written."""
+    if _native is not None and out is None and stream is None and not accumulate:
+        r = _native.product(1, dy, w, offsets, None, None, out_dtype)
+        if r is not None:
+            return r if type(r) is not int else _failed(r, "nvfp4_moe_grouped_gemm_dx")
     dtype, index = dy.dtype, dy.get_device()
     t = _TYPES.get(dtype, TYPE_F32)
     if index < 0 or t > TYPE_F16 or w.dtype is not dtype:
@@ -289,6 +326,10 @@ def grouped_gemm_dw(dy, x, offsets=None, *, out=None, out_dtype=None, accumulate
     """The gradient of grouped_gemm for w: dW_e = sum over the rows p of e of dy[p]^T x[p].
     dy: [rows][n], x: [rows][k], both bf16 or f16. out: [groups][n][k] ([n][k] without
     offsets), f32 by default; zeros for a group without rows. accumulate: out += (f32)."""
+    if _native is not None and out is None and stream is None and not accumulate:
+        r = _native.product(2, dy, x, offsets, None, None, out_dtype)
+        if r is not None:
+            return r if type(r) is not int else _failed(r, "nvfp4_moe_grouped_gemm_dw")
     dtype, index = x.dtype, x.get_device()
     t = _TYPES.get(dtype, TYPE_F32)
     if index < 0 or t > TYPE_F16 or dy.dtype is not dtype:

@@ -636,6 +636,39 @@ print("ok")
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
 
 
+def test_both_bindings_make_the_same_calls(monkeypatch):
+    """The native marshalling of the common calls and the Python one behind it: the same outputs, types and strides,
+    and what one does not take the other does or refuses."""
+    P = nv.products
+    run, (x, dy, w) = _all_calls(rows=210, n=77, k=134, seed=183)
+    run()
+    assert P._native is not None, "_marshal.so is not built"
+    native = run()
+    q, s = native[:2]
+    off = offsets_of((0, 1, 170, 39))
+    taken = P._native.product(0, x, w, off, None, None, None)
+    assert taken.dtype == BF16 and tuple(taken.shape) == (210, 77) and taken.stride(0) == 80
+    assert P._native.product(0, x, w, None, None, None, None) is None          # four matrices, no offsets
+    assert P._native.product(0, x, w, off.long(), None, None, None) is None
+    assert P._native.product(0, x.t(), w, off, None, None, None) is None
+    assert P._native.product(0, x, w, off, s, s, None) is None                 # scales without codes
+    assert P._native.product(0, q, w, off, None, None, None) is None           # two types
+    assert P._native.product(0, x.cpu(), w, off, None, None, None) is None
+    assert P._native.product(1, q, q, None, None, None, None) is None
+    assert P._native.product(3, x, w, off, None, None, None) is None
+    assert P._native.product(0, "x", w, off, None, None, None) is None
+    assert P._native.product(0, x, w, off, None, None, torch.int8) is None
+    assert P._native.quantize(q, False) is None and P._native.quantize(x[:, :7], True) is None
+    with pytest.raises(nv.NVFP4MoEError):       # rows that do not start every 16 bytes: the library's own refusal
+        nv.grouped_gemm(x[:, 1:], w[:, :, 1:], off)
+    monkeypatch.setattr(P, "_native", None)
+    monkeypatch.setattr(P, "_marshal", None)
+    for a, b in zip(native, run()):
+        assert torch.equal(a, b) and a.dtype == b.dtype and a.stride() == b.stride()
+    with pytest.raises(nv.NVFP4MoEError):
+        nv.grouped_gemm(x[:, 1:], w[:, :, 1:], off)
+
+
 def test_calls_from_several_threads():
     import threading
     run, _ = _all_calls(rows=200, n=264, k=328, seed=181)
