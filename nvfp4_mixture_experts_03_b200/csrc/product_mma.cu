@@ -375,6 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&map_a);
         tma_prefetch_desc(&map_b);
     }
+    // Barriers, TMEM and descriptors are ready; what follows reads what may come from the
+    // kernel before.
+    start_after_previous();
     if (!q.p.offsets) {   // one group of all rows
         if (threadIdx.x == 0) {
             groups.lo[0] = groups.before[0] = 0;
@@ -957,17 +960,19 @@ MmaKernel kernel_of(int mode, bool i8, int cg, bool f32, bool split) {
     return f32 ? kernel_of<1, true, false>(mode, i8) : kernel_of<1, false, false>(mode, i8);
 }
 
+// attr: two of them.
 cudaLaunchConfig_t config(int grid, int cluster, size_t smem, cudaStream_t s, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = cluster;
-    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    set_programmatic(&attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cfg;
 }
 
@@ -996,13 +1001,13 @@ cudaError_t resident(Resident *out) {
         }
         e = cudaDeviceGetAttribute(&r.ctas, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return e;
-        cudaLaunchAttribute attr;
-        const cudaLaunchConfig_t cfg = config(2, 2, kSmemLimit, 0, &attr);
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = config(2, 2, kSmemLimit, 0, attr);
         e = cudaOccupancyMaxActiveClusters(&r.pairs, kernel_of(kFwd, false, 2, false, false), &cfg);
         if (e != cudaSuccess) return e;
         if (r.pairs < 1) return cudaErrorInvalidConfiguration;
         for (int n = 2; n <= 8; n *= 2) {
-            const cudaLaunchConfig_t c = config(n, n, kSmemLimit, 0, &attr);
+            const cudaLaunchConfig_t c = config(n, n, kSmemLimit, 0, attr);
             e = cudaOccupancyMaxActiveClusters(&r.split[n], kernel_of(kFwd, false, 1, false, true), &c);
             if (e != cudaSuccess) return e;
         }
@@ -1101,9 +1106,9 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     // no more CTAs than there can be tiles
     const int64_t most = std::max<int64_t>(most_tiles(mode, p, cols, shape), 1);
     const int units = (int)std::min<int64_t>(q.split > 1 ? r.split[q.split] : cg == 2 ? r.pairs : r.ctas, most);
-    cudaLaunchAttribute attr;
+    cudaLaunchAttribute attr[2];
     const int cluster = cg * q.split;
-    const cudaLaunchConfig_t cfg = config(units * cluster, cluster, smem_bytes(q.bn, cg, q.stages, p.groups), s, &attr);
+    const cudaLaunchConfig_t cfg = config(units * cluster, cluster, smem_bytes(q.bn, cg, q.stages, p.groups), s, attr);
     return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg, out == NVFP4_MOE_TYPE_F32, q.split > 1), q, a, b, b_small, o);
 }
 

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) produ
     constexpr bool kI8 = std::is_same<T, int8_t>::value;
     using Acc = typename std::conditional<kI8, int32_t, float>::type;
     __shared__ Acc part[kWarps][8 * NT][kCols + 1];
+    start_after_previous();
     const int col0 = blockIdx.x * kCols;
     // Rows row0 .. row0+nrow-1 of group e: with offsets, block y stands for row y and works
     // if that row opens a batch of 8 * NT rows of its group.

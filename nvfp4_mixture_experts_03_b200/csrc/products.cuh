@@ -41,6 +41,20 @@ __device__ inline __half from_f32(float v) { return __float2half_rn(v); }
 template <>
 __device__ inline float from_f32(float v) { return v; }
 
+// The products follow one another in short chains, and a small one's launch and start take
+// as long as its work: each is a programmatic dependent of the kernel before it in the
+// stream, lets its own dependents launch at once, and waits for that kernel, all of it,
+// before it touches global memory. Every CTA has to wait, even one without work: the next
+// kernel relies on this one's end for the ends of all before it.
+__device__ inline void start_after_previous() {
+    grid_dep_launch();
+    grid_dep_wait();
+}
+inline void set_programmatic(cudaLaunchAttribute *attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+}
+
 // A launch that reports its own error, and none that was pending before it.
 template <typename... P, typename... A>
 cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, const A &...args) {
@@ -48,6 +62,10 @@ cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, int threads, cudaStre
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.stream = s;
+    cudaLaunchAttribute attr;
+    set_programmatic(&attr);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 

@@ -189,6 +189,7 @@ __device__ inline void code_chunk(const Chunk<T, kSwiglu> &k, float scale, float
 template <typename T, bool kSwiglu, bool kVec, int kPer, int kKeep>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const nvfp4_moe_quantize_io io) {
     __shared__ uint32_t part[kThreads / 32];
+    start_after_previous();
     const int row = kPer == 32 ? blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (kPer == 32 && row >= io.rows) return;
     const int me = threadIdx.x & (kPer - 1);

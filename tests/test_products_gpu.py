@@ -636,6 +636,85 @@ print("ok")
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
 
 
+def _chain(steps, sync, layer):
+    """Calls that each read what the one before wrote, through buffers that are written again and again; the
+    routed layer's decode kernel and torch's own among them."""
+    done = torch.cuda.synchronize if sync else (lambda: None)
+    E, H, I = 4, 256, 192
+    w, wq = normal((E, I, H), BF16, 201, 0.06), codes((H, I), 202)
+    w2, ws = normal((E, I, H), BF16, 203, 0.06), torch.full((H,), 4e-4, device=DEV)
+    x = normal((60, H), F32, 204)
+    xb, h = torch.empty(60, H, dtype=BF16, device=DEV), torch.empty(60, I, dtype=BF16, device=DEV)
+    q, s = torch.empty(60, I, dtype=torch.int8, device=DEV), torch.empty(60, device=DEV)
+    dx, dw = torch.empty(60, H, dtype=BF16, device=DEV), torch.empty(E, I, H, device=DEV)
+    logits, square = torch.randn(4, 8, generator=gen(205), device=DEV), codes((H, H), 206)
+    off, small = offsets_of((9, 0, 40, 11)), offsets_of((1, 0, 2, 1))
+    xq, xs = torch.empty(4, H, dtype=torch.int8, device=DEV), torch.empty(4, device=DEV)
+    out = torch.empty(4, H, device=DEV)
+    for _ in range(steps):
+        xb.copy_(x); done()
+        nv.grouped_gemm(xb, w, off, out=h); done()
+        nv.grouped_gemm(xb[:4], w, small, out=h[:4]); done()          # streamed
+        nv.quantize_int8(h, q=q, scale=s); done()
+        nv.gemm_int8(q, wq, s, ws, out=x, accumulate=True); done()
+        nv.grouped_gemm_dx(h, w2, off, out=dx); done()
+        nv.grouped_gemm_dw(h, xb, off, out=dw); done()
+        nv.quantize_int8(dx[:4], q=xq, scale=xs); done()
+        layer.forward(xq, x_scale=xs, logits=logits, out=out); done()
+        nv.gemm_int8(xq, square, xs, ws, out=out, accumulate=True); done()
+        x.mul_(0.5)
+        x[:4].add_(out, alpha=1e-3); done()
+    torch.cuda.synchronize()
+    return [t.clone() for t in (x, h, q, s, dx, dw, xq, xs, out)]
+
+
+def test_chains_of_dependent_calls():
+    """A kernel may start before the one ahead of it has ended, but touches nothing until then: a chain without a
+    wait gives the bits of one that waits after every call; so does its capture, replayed."""
+    import synth
+    dims = synth.LayerDims(E=8, H=256, I=128, K=2)
+    layer = nv.MoELayer.from_layer(synth.make_layer(dims, seed=9).to(DEV), top_k=dims.K, max_tokens=4)
+    want = _chain(25, True, layer)
+    for _ in range(4):
+        for a, b in zip(_chain(25, False, layer), want):
+            assert torch.equal(a, b)
+    assert layer.status() == 0
+    layer.close()
+
+
+def test_captured_across_two_streams():
+    x, w = normal((300, 256), BF16, 211), normal((2, 320, 256), BF16, 212, 0.1)
+    off = offsets_of((100, 200))
+    y, z, u = (torch.empty(300, n, dtype=BF16, device=DEV) for n in (320, 256, 320))
+
+    def run(side):
+        main = torch.cuda.current_stream()
+        nv.grouped_gemm(x, w, off, out=y)
+        side.wait_stream(main)
+        nv.grouped_gemm_dx(y, w, off, out=z, stream=side)
+        q, s = nv.quantize_int8(y)
+        main.wait_stream(side)
+        nv.grouped_gemm(z, w, off, out=u)
+        return q, s
+
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    run(side)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        q, s = run(side)
+    for seed in (1, 2, 3):
+        x.copy_(torch.randn(*x.shape, generator=gen(213 + seed), device=DEV))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (y, z, u, q, s)]
+        nv.grouped_gemm(x, w, off, out=y); torch.cuda.synchronize()
+        nv.grouped_gemm_dx(y, w, off, out=z); torch.cuda.synchronize()
+        nv.grouped_gemm(z, w, off, out=u); torch.cuda.synchronize()
+        want = [y, z, u, *nv.quantize_int8(y)]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_both_bindings_make_the_same_calls(monkeypatch):
     """The native marshalling of the common calls and the Python one behind it: the same outputs, types and strides,
     and what one does not take the other does or refuses."""
