@@ -402,13 +402,6 @@ __device__ inline int h_exp_for(float amax) {
     return e < -100 ? -100 : e;
 }
 
-// ------------------------------------------------------------ tensor maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_fn();   // the driver's cuTensorMapEncodeTiled, or null
-
 // ------------------------------------------------------------ kernel decls
 void launch_route_large(const Params &p, cudaStream_t s);
 void launch_prep_prefill(const Params &p, cudaStream_t s);

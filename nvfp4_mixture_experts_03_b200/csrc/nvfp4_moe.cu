@@ -15,6 +15,7 @@
 #include <new>
 
 #include "common.cuh"
+#include "tensor_map.cuh"
 
 using namespace nvmoe;
 

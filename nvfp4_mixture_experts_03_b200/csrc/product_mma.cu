@@ -26,6 +26,7 @@
 #include <mutex>
 
 #include "products.cuh"
+#include "tensor_map.cuh"
 
 namespace nvmoe {
 namespace {
