@@ -33,7 +33,10 @@
  * device that can reach the pointers). Calls keep nothing from one to the next and may
  * run concurrently, on any streams and threads, as long as their outputs are disjoint;
  * all of them can be captured into graphs. Results do not depend on timing: the same
- * inputs give the same bits on every run.
+ * inputs give the same bits on every run. Every kernel is launched as a programmatic
+ * dependent of the one before it in the stream and waits for all of it before it touches
+ * memory; it lets a programmatic dependent that follows start at once, so such a kernel of
+ * the caller's has to wait (griddepcontrol.wait) before it reads what these calls write.
  */
 #ifndef NVFP4_MOE_PRODUCTS_H
 #define NVFP4_MOE_PRODUCTS_H

@@ -192,7 +192,7 @@ cudaError_t launch(const Product &p, nvfp4_moe_type out, cudaStream_t s) {
 bool product_streams(int mode, const Product &p, int elem_bytes) {
     if (mode != kFwd) return false;
     const int64_t blocks = cdiv(p.n, kCols);
-    if (p.offsets) return p.rows * blocks <= 3072;
+    if (p.offsets) return p.rows * blocks <= 3100;
     if (p.rows <= 8) return true;
     const int64_t passes = cdiv(p.rows, 32);
     return passes * blocks <= 512 && passes * p.n * p.k * elem_bytes <= 30000000;
