@@ -48,6 +48,13 @@ NVFP4_MOE_API int nvfp4_moe_test_last_detail(const nvfp4_moe_t *h);
  * thread-safe. */
 NVFP4_MOE_API void nvfp4_moe_test_fail_alloc(int32_t n);
 
+/* Products (nvfp4_moe_products.h) that take the tensor-core tiles: the first CTA of each of
+ * the next n launches leaves out its copies, so every wait on them runs out (after about 2 s),
+ * the call latches NVFP4_MOE_ERR_TIMEOUT for nvfp4_moe_products_status and its output is not
+ * complete; later calls are correct again. n <= 0 disarms it. Process-wide; not
+ * thread-safe. */
+NVFP4_MOE_API void nvfp4_moe_test_products_stall(int32_t n);
+
 #ifdef __cplusplus
 }
 #endif

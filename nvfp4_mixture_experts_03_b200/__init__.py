@@ -36,7 +36,7 @@ EXPORTS = ("nvfp4_moe_create", "nvfp4_moe_workspace_bytes", "nvfp4_moe_forward",
            "nvfp4_moe_forward_decode_static", "nvfp4_moe_forward_decode_stack",
            "nvfp4_moe_test_set_flags", "nvfp4_moe_test_fail_alloc", "nvfp4_moe_test_last_detail",
            "nvfp4_moe_quantize_int8", "nvfp4_moe_grouped_gemm", "nvfp4_moe_grouped_gemm_dx",
-           "nvfp4_moe_grouped_gemm_dw", "nvfp4_moe_products_status")
+           "nvfp4_moe_grouped_gemm_dw", "nvfp4_moe_products_status", "nvfp4_moe_test_products_stall")
 TEST_DECODE_STALL = 1   # include/nvfp4_moe_test.h
 TEST_NO_SMALL = 2       # every used expert takes the grouped-GEMM tiles
 PHASE_EVENTS = 5
@@ -316,4 +316,4 @@ def debug_buffers(T: int, E: int, K: int, device) -> dict:
 from .products import (GemmIO, QuantizeIO, gemm_int8, grouped_gemm, grouped_gemm_dw,  # noqa: E402,F401
                        grouped_gemm_dx, nvfp4_moe_grouped_gemm, nvfp4_moe_grouped_gemm_dw,
                        nvfp4_moe_grouped_gemm_dx, nvfp4_moe_products_status, nvfp4_moe_quantize_int8,
-                       products_status, quantize_int8)
+                       nvfp4_moe_test_products_stall, products_status, quantize_int8)

@@ -58,6 +58,7 @@ struct MmaParams {
     int32_t stages;
     int32_t split;         // one-CTA tiles: CTAs of a cluster that share a tile's sum (1: none)
     int32_t staged;        // whole batches of outputs leave as boxes (map_o is set); rows are 16-byte aligned
+    int32_t stall;         // test hook: the first CTA makes no copies
     int32_t a_whole, b_whole;   // M- or N-major operands: all of a stage's 64-column boxes as one
 };
 
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kTmaWarp) {
         // ------------------------------------------------------------ TMA
         uint32_t issued = 0, issued_phase = 0;   // stages loaded, and the parity of their last use
-        bool ok = true;
+        bool ok = !(q.stall && blockIdx.x == 0);
         const bool elected = elect_one();
         while (ok) {
             const OutTile t = next_tile();
@@ -1018,6 +1019,8 @@ cudaError_t resident(Resident *out) {
     return cudaSuccess;
 }
 
+int32_t g_stall = 0;   // test hook: launches to come that stall
+
 // The tile shape: CTAs to a tile, its most rows, and CTAs that share its sum.
 struct Shape {
     int cg, bn, split;
@@ -1094,7 +1097,8 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     q.a_whole = mode != kFwd && oa.cols % 64 == 0;
     q.b_whole = mode == kDw && ob.cols % 64 == 0 && p.n % (64 * cg) == 0;
     const int64_t out_rows = mode == kDw ? (int64_t)p.groups * p.n : p.rows;
-    q.staged = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.out_ld % (out == NVFP4_MOE_TYPE_F32 ? 4 : 8) == 0 && !p.out_add;
+    q.staged = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.out_ld % (out == NVFP4_MOE_TYPE_F32 ? 4 : 8) == 0 &&
+               p.out_ld < (int64_t(1) << 37) && !p.out_add;   // (a tensor map's strides end at 2^40 bytes)
     CUtensorMap a, b, b_small, o;
     bool ok = map_operand(&a, oa, type, mode == kFwd ? 128 : 64, q.a_whole ? 2 : 0);
     b = b_small = o = a;   // where they are not used
@@ -1104,6 +1108,10 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     if (ok && q.staged) ok = map_output(&o, p.out, out, out_rows, cols, p.out_ld);
     if (!ok) return cudaErrorInvalidValue;
     q.split = shape.split;
+    if (g_stall > 0) {
+        g_stall--;
+        q.stall = 1;
+    }
     // no more CTAs than there can be tiles
     const int64_t most = std::max<int64_t>(most_tiles(mode, p, cols, shape), 1);
     const int units = (int)std::min<int64_t>(q.split > 1 ? r.split[q.split] : cg == 2 ? r.pairs : r.ctas, most);
@@ -1112,6 +1120,8 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     const cudaLaunchConfig_t cfg = config(units * cluster, cluster, smem_bytes(q.bn, cg, q.stages, p.groups), s, attr);
     return cudaLaunchKernelEx(&cfg, kernel_of(mode, i8, cg, out == NVFP4_MOE_TYPE_F32, q.split > 1), q, a, b, b_small, o);
 }
+
+void test_product_stall(int n) { g_stall = std::max(n, 0); }
 
 int product_status(cudaStream_t s) {
     int32_t st[kStatusWords];

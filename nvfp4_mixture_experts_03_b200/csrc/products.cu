@@ -107,6 +107,8 @@ int nvfp4_moe_grouped_gemm(const nvfp4_moe_gemm_io *io, void *stream) { return p
 int nvfp4_moe_grouped_gemm_dx(const nvfp4_moe_gemm_io *io, void *stream) { return product(kDx, io, stream); }
 int nvfp4_moe_grouped_gemm_dw(const nvfp4_moe_gemm_io *io, void *stream) { return product(kDw, io, stream); }
 
+void nvfp4_moe_test_products_stall(int32_t n) { test_product_stall(n); }
+
 int nvfp4_moe_products_status(void *stream) {
     if (const int rc = check_device()) return rc;
     return product_status(static_cast<cudaStream_t>(stream));

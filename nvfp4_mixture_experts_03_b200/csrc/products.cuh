@@ -74,6 +74,7 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
                                cudaStream_t s);
 bool product_streams(int mode, const Product &p, int elem_bytes);   // few enough rows to be streamed
 cudaError_t launch_product_stream(const Product &p, nvfp4_moe_type type, nvfp4_moe_type out_type, cudaStream_t s);
+void test_product_stall(int n);       // test hook (nvfp4_moe_test.h)
 int product_status(cudaStream_t s);   // the first wait that gave up on the current device, cleared
 
 }  // namespace nvmoe

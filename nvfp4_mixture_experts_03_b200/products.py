@@ -63,6 +63,11 @@ def nvfp4_moe_products_status(stream: int) -> int:
     return lib().nvfp4_moe_products_status(C.c_void_p(stream))
 
 
+def nvfp4_moe_test_products_stall(n: int) -> None:
+    """Test hook (include/nvfp4_moe_test.h): waits of the next n tile launches run out."""
+    lib().nvfp4_moe_test_products_stall(C.c_int32(n))
+
+
 def products_status(stream=None) -> int:
     """Synchronises and returns the first device-side error of the products on the current
     device since the last read (0 if none), clearing it."""

@@ -748,6 +748,26 @@ def test_both_bindings_make_the_same_calls(monkeypatch):
         nv.grouped_gemm(x[:, 1:], w[:, :, 1:], off)
 
 
+@pytest.mark.parametrize("call,counts,n,k", [
+    ("fwd", (200, 300), 200, 264), ("dx", (16384,), 512, 512), ("dw", (1001,) * 8, 1024, 1024), ("dw", (9000,), 96, 136),
+], ids=["one CTA", "a pair", "a pair with rows to zero", "a split sum"])
+def test_a_wait_that_runs_out_is_reported(call, counts, n, k):
+    """The first CTA's copies are left out by the test hook: the bounded waits end (about 2 s), the status says so once,
+    and the next call is whole again."""
+    off, rows, E = offsets_of(counts), sum(counts), len(counts)
+    x, dy, w = normal((rows, k), BF16, 221), normal((rows, n), BF16, 222), normal((E, n, k), BF16, 223, 0.1)
+    run = {"fwd": lambda: nv.grouped_gemm(x, w, off), "dx": lambda: nv.grouped_gemm_dx(dy, w, off),
+           "dw": lambda: nv.grouped_gemm_dw(dy, x, off)}[call]
+    want = run()
+    assert nv.products_status() == 0
+    nv.nvfp4_moe_test_products_stall(1)
+    run()
+    assert nv.products_status() == -8
+    assert nv.products_status() == 0
+    assert torch.equal(run(), want)
+    assert nv.products_status() == 0
+
+
 def test_calls_from_several_threads():
     import threading
     run, _ = _all_calls(rows=200, n=264, k=328, seed=181)
