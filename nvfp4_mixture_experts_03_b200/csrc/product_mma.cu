@@ -377,9 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&map_a);
         tma_prefetch_desc(&map_b);
     }
-    // Barriers, TMEM and descriptors are ready; what follows reads what may come from the
-    // kernel before.
-    start_after_previous();
+    // Barriers, TMEM and descriptors are ready; offsets may come from the kernel before.
+    // Without them only the copying and the epilogue warps touch global memory, and wait.
+    grid_dep_launch();
+    if (q.p.offsets) grid_dep_wait();
     if (!q.p.offsets) {   // one group of all rows
         if (threadIdx.x == 0) {
             groups.lo[0] = groups.before[0] = 0;
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ TMA
         uint32_t issued = 0, issued_phase = 0;   // stages loaded, and the parity of their last use
         bool ok = !(q.stall && blockIdx.x == 0);
+        if (!q.p.offsets) grid_dep_wait();
         const bool elected = elect_one();
         while (ok) {
             const OutTile t = next_tile();
@@ -665,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // columns of 16 bits, or for a whole batch of 32
         const bool storer = quarter < (kF32 ? 1 : 2) && lane == 0;
         uint8_t *os = out_stage + half * kOutBytes;
+        if (!q.p.offsets) grid_dep_wait();
         while (true) {
             const OutTile t = next_tile();
             // zeros: an expert without rows, or a part of a short sum
@@ -1037,7 +1040,7 @@ int64_t most_tiles(int mode, const Product &p, int cols, const Shape &s) {
 // with N columns takes about max(380, 3.7 N) cycles in one CTA and max(400, 2.75 N) in a pair
 // (all SMs busy, operands in L2), 32 columns of an epilogue 420 (16 bits); a tile costs 1200
 // besides, a pair 2000 once. Small tiles fill the GPU where there are few rows (201 rows x
-// 2048 x 768 int8: 6.4 us in tiles of 64, 9.7 in pairs of 256), pairs of 256 move the fewest
+// 2048 x 768 int8, before launches overlapped: 6.4 us in tiles of 64, 9.7 in pairs of 256), pairs of 256 move the fewest
 // bytes an MMA (4096 x 2560 x 2560 BF16: 44 us, 69 in tiles of 64; 64 experts, 16384 pairs,
 // dx: 121 us, 131 in tiles of 64). Few tiles of long sums are split over clusters, whose
 // join costs about 4500 cycles (dw of one group, 10000 rows, 200 x 304: 43 us whole, 12 in eight
