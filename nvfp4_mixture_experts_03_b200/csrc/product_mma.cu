@@ -63,7 +63,7 @@ struct MmaParams {
 };
 
 constexpr int kBoxSmall = 32;           // rows of the smaller K-major B box
-constexpr int kOutBytes = 16 * 1024;    // a half's staged outputs: 64 rows x 128 columns of 16 bits, 32 of 32
+constexpr int kOutBytes = 4 * 1024;     // a warp's staged outputs: 64 rows x 32 columns of 16 bits, 32 rows of 32 bits
 
 struct __align__(16) Bars {
     uint64_t full[kMaxStages];    // leader: an arrival for each CTA of the group, and all their bytes
@@ -107,7 +107,7 @@ inline size_t groups_bytes(int groups) {
 
 inline size_t stage_bytes(int bn, int cg) { return kABytes + (size_t)bn / cg * kLine; }
 inline size_t smem_bytes(int bn, int cg, int stages, int groups) {
-    return 1024 + stages * stage_bytes(bn, cg) + 2 * kOutBytes + sizeof(Bars) + groups_bytes(groups);
+    return 1024 + stages * stage_bytes(bn, cg) + kEpiWarps * kOutBytes + sizeof(Bars) + groups_bytes(groups);
 }
 
 template <int CG>
@@ -144,11 +144,16 @@ __device__ inline void tma_4d(void *dst, const CUtensorMap *map, uint64_t *bar, 
             : "memory");
 }
 
-// Bulk tensor store of an output box.
+// Bulk tensor store of an output box, a group of its own.
 __device__ inline void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n cp.async.bulk.commit_group;" ::"l"(map),
                  "r"(smem_u32(src)), "r"(x), "r"(y)
                  : "memory");
+}
+// What this warp staged before has been read.
+__device__ inline void left_stage(int lane) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
 }
 
 // 16 lanes x 32 columns as fragments: registers 4i..4i+3 hold, of columns 8i + 2 (lane % 4)
@@ -176,20 +181,6 @@ __device__ inline uint32_t pack_bf16(float lo, float hi) {
 __device__ inline uint32_t pack_f16(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-__device__ inline void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-
-// Named barrier of the four epilogue warps that share a staging buffer.
-__device__ inline void half_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
-
-__device__ inline bool half_all(int half, bool v) {
-    uint32_t r;
-    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.and.pred q, %1, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
-                 : "=r"(r)
-                 : "r"(1 + half), "r"((uint32_t)v)
-                 : "memory");
-    return r != 0;
 }
 
 template <int CG, bool kI8>
@@ -342,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t b_bytes = (uint32_t)q.bn / CG * kLine, stage_size = kABytes + b_bytes;
     uint8_t *out_stage = smem + q.stages * stage_size;
-    Bars *bars = reinterpret_cast<Bars *>(out_stage + 2 * kOutBytes);
+    Bars *bars = reinterpret_cast<Bars *>(out_stage + kEpiWarps * kOutBytes);
     const Groups groups(bars + 1, q.p.groups);
     volatile int *abort = &bars->abort;
 
@@ -655,24 +646,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kEpiWarps) {
         // -------------------------------------------------------- epilogue
         // The eight warps are two halves of four, one warp of each to a quarter of the TMEM
-        // lanes (32 output columns); the halves take batches of kBatch output rows in turn,
-        // each with a staging buffer of its own. Shared memory is what the MMAs run on (each
-        // stage's bytes pass it twice in the time of its MMAs) and a short sum leaves little
-        // time between two tiles, so what counts is how few passes and waits a batch takes.
+        // lanes (32 output columns); the halves take batches of kBatch output rows in turn.
+        // Shared memory is what the MMAs run on (each stage's bytes pass it twice in the time
+        // of its MMAs) and a short sum leaves little time between two tiles, so what counts is
+        // how few passes and waits a batch takes: each warp stages and stores for itself,
+        // without a barrier (with four warps to a buffer and its stores 13615 x 2560 x 128 int8
+        // took 21.7 us instead of 18.9, dw of 512 experts of 256 x 256 to FP32 38.6 instead of
+        // 32.6; but 805 MB of FP32 185 instead of 201).
         constexpr int kBatch = kF32 ? 32 : 64, kBatches = kAccCols / (2 * kBatch);
         uint32_t acc_phase = 0, it = 0;
         const int cols = MODE == kFwd ? q.p.n : q.p.k;
         const int quarter = warp & 3, half = warp >> 2;
-        // issue this half's bulk stores (some 300 cycles each for the thread): one for each 64
-        // columns of 16 bits, or for a whole batch of 32
-        const bool storer = quarter < (kF32 ? 1 : 2) && lane == 0;
-        uint8_t *os = out_stage + half * kOutBytes;
+        uint8_t *os = out_stage + warp * kOutBytes;   // [row][32 columns]
         if (!q.p.offsets) grid_dep_wait();
         while (true) {
             const OutTile t = next_tile();
             // zeros: an expert without rows, or a part of a short sum
             const bool none = (MODE == kDw || kSplit) && t.e >= 0 && t.c == 0;
-            const int col0 = t.m0 + rank * 128, col = col0 + 32 * quarter + lane;   // of the CTA, of this lane
+            const int col0 = t.m0 + rank * 128 + 32 * quarter, col = col0 + lane;   // of the warp, of this lane
             const int64_t orow = (MODE == kDw ? (int64_t)t.e * q.p.n : 0) + t.row0;
             // Scales of int8 products come in while the sums are still being formed: of the
             // columns and rows that a fragment gives this lane, or of its column and row.
@@ -680,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kI8 && t.e >= 0) {
                 const float *ws = q.p.w_scale + (int64_t)t.e * q.p.n, *xs = q.p.x_scale + t.row0;
 #pragma unroll
-                for (int j = 0; j < 4; j++) cs[j] = ws[min(kF32 ? col : col - lane + 8 * j + (lane >> 2), cols - 1)];
+                for (int j = 0; j < 4; j++) cs[j] = ws[min(kF32 ? col : col0 + 8 * j + (lane >> 2), cols - 1)];
 #pragma unroll
                 for (int h = 0; h < kBatches; h++)
 #pragma unroll
@@ -688,10 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         rs[h][j] = xs[min(kBatch * (2 * h + half) + (kF32 ? lane : 8 * (j >> 1) + 2 * (lane & 3) + (j & 1)), t.nrow - 1)];
             }
             const int buf = it & 1;
-            // the four warps that share a staging buffer leave together, or not at all
-            bool go = t.e >= 0;
-            if (go && !none) go = mbar_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, g_status, 5);
-            if (!half_all(half, go)) break;
+            if (t.e < 0 || (!none && !warp_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, 5))) break;
             if (none && q.p.out_add && !kSplit) continue;
             if (!none) {
                 it++;
@@ -744,26 +732,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             w[i][j] = none ? 0u : q.out_type == NVFP4_MOE_TYPE_BF16 ? pack_bf16(v0, v1) : pack_f16(v0, v1);
                         }
-                    if (storer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    half_sync(half);   // the previous batch has left
-                    // [64 columns' half][row][128 bytes] in the 128-byte swizzle
-                    const int piece = 4 * quarter + (lane >> 3), k = lane & 7;
-                    uint8_t *to = os + (piece >> 3) * (kOutBytes / 2) + k * 128 + (((piece & 7) ^ k) << 4);
+                    left_stage(lane);
+                    // 64 bytes a row, in the 64-byte swizzle
+                    const int k = lane & 7;
+                    uint8_t *to = os + k * 64 + (((lane >> 3) ^ (k >> 1)) << 4);
 #pragma unroll
-                    for (int i = 0; i < 8; i++) stmatrix_trans(to + i * 8 * 128, w[i]);
-                    if (q.staged && n == kBatch) {   // whole boxes
+                    for (int i = 0; i < 8; i++) stmatrix_trans(to + i * 8 * 64, w[i]);
+                    if (q.staged && n == kBatch) {   // a whole box
                         fence_proxy_async_smem();
-                        half_sync(half);
-                        if (storer && col0 + 64 * quarter < cols) {
-                            tma_store_2d(&map_o, os + quarter * (kOutBytes / 2), col0 + 64 * quarter, (int)(orow + r));
-                            bulk_commit();
-                        }
+                        __syncwarp();
+                        if (lane == 0 && col0 < cols) tma_store_2d(&map_o, os, col0, (int)(orow + r));
                     } else {   // a group's end, or rows that a box cannot have: 16 bytes at a time
-                        half_sync(half);
-                        for (int i = 32 * quarter + lane; i < n * 16; i += 128) {
-                            const int row = i >> 4, pc = i & 15, c0 = col0 + 8 * pc;
-                            const uint4 v = *reinterpret_cast<const uint4 *>(os + (pc >> 3) * (kOutBytes / 2) + row * 128 +
-                                                                             (((pc & 7) ^ (row & 7)) << 4));
+                        __syncwarp();
+                        for (int i = lane; i < n * 4; i += 32) {
+                            const int row = i >> 2, pc = i & 3, c0 = col0 + 8 * pc;
+                            const uint4 v = *reinterpret_cast<const uint4 *>(os + row * 64 + ((pc ^ ((row >> 1) & 3)) << 4));
                             uint16_t *o = static_cast<uint16_t *>(q.p.out) + (orow + r + row) * q.p.out_ld + c0;
                             if (q.staged && c0 + 8 <= cols)
                                 *reinterpret_cast<uint4 *>(o) = v;
@@ -790,17 +773,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                : kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs[h][0], j) * cs[0])
                                      : __uint_as_float(u[j]);
                     if (q.staged && n == kBatch) {
-                        if (storer) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        half_sync(half);
-                        float *to = reinterpret_cast<float *>(os) + 32 * quarter + lane;   // [row][128 columns]
+                        left_stage(lane);
+                        float *to = reinterpret_cast<float *>(os) + lane;
 #pragma unroll
-                        for (int j = 0; j < 32; j++) to[128 * j] = v[j];
+                        for (int j = 0; j < 32; j++) to[32 * j] = v[j];
                         fence_proxy_async_smem();
-                        half_sync(half);
-                        if (storer && col0 < cols) {
-                            tma_store_2d(&map_o, os, col0, (int)(orow + r));
-                            bulk_commit();
-                        }
+                        __syncwarp();
+                        if (lane == 0 && col0 < cols) tma_store_2d(&map_o, os, col0, (int)(orow + r));
                     } else if (col < cols) {   // a warp has 128 bytes of a row as it is
                         float *o = static_cast<float *>(q.p.out) + (orow + r) * q.p.out_ld + col;
                         if (q.p.out_add) {
@@ -817,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (storer) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     if constexpr (kSplit) {
@@ -937,16 +916,16 @@ bool map_operand(CUtensorMap *m, const Operand &o, nvfp4_moe_type type, int rows
            CUDA_SUCCESS;
 }
 
-// Output rows as a store target: 16 bits in boxes of 64 columns x 64 rows in the 128-byte
-// swizzle, 32 bits in plain boxes of 128 columns x 32 rows.
+// Output rows as a store target: 16 bits in boxes of 32 columns x 64 rows in the 64-byte
+// swizzle, 32 bits in plain boxes of 32 columns x 32 rows.
 bool map_output(CUtensorMap *m, void *base, nvfp4_moe_type type, int64_t rows, int64_t cols, int64_t ld) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const bool f32 = type == NVFP4_MOE_TYPE_F32;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)(ld * (f32 ? 4 : 2))};
-    const cuuint32_t box[2] = {f32 ? 128u : 64u, f32 ? 32u : 64u}, ones[2] = {1, 1};
+    const cuuint32_t box[2] = {32, f32 ? 32u : 64u}, ones[2] = {1, 1};
     return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : map_type(type), 2, base, dims, strides, box, ones,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
