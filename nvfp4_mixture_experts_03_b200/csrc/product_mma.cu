@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&map_b);
     }
     // Barriers, TMEM and descriptors are ready; offsets may come from the kernel before.
-    // Without them only the copying and the epilogue warps touch global memory, and wait.
+    // Without them the wait for it comes later, when the first tiles are being listed.
     grid_dep_launch();
     if (q.p.offsets) grid_dep_wait();
     if (!q.p.offsets) {   // one group of all rows
@@ -447,6 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (CG == 2) cluster_sync_all();   // both CTAs' barriers initialised and TMEM allocated
     tc_fence_after();
     const uint32_t tmem_base = bars->tmem_slot;
+    // Dense calls wait for the kernel before here, all warps but the tile warp, which lists the
+    // first tiles meanwhile: before any wait of a bounded time, whose clock would else run while
+    // that kernel does (one with more than two seconds left, or one that gives up itself, would
+    // take this call with it).
+    if (!q.p.offsets && warp != kTileWarp) grid_dep_wait();
     // The next tile, listed by the tile warp (finding it takes a few integer divisions: about
     // a thousand cycles that no other warp should spend between two tiles). e is -1 past
     // the last one, and after a wait that gave up.
@@ -480,7 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ TMA
         uint32_t issued = 0, issued_phase = 0;   // stages loaded, and the parity of their last use
         bool ok = !(q.stall && blockIdx.x == 0);
-        if (!q.p.offsets) grid_dep_wait();
         const bool elected = elect_one();
         while (ok) {
             const OutTile t = next_tile();
@@ -634,6 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t.c0 += from;
                 t.c = max(0, min(t.c - from, per * kStep));
             }
+            // (the first kTilesAhead slots are free: no wait on the clock)
+            if (!q.p.offsets && round == kTilesAhead) grid_dep_wait();
             if (!warp_wait<false>(&bars->tile_empty[slot], slot_phase ^ 1, abort, 8)) break;
             if (lane == 0) {
                 groups.ahead[slot] = t;
@@ -658,7 +664,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cols = MODE == kFwd ? q.p.n : q.p.k;
         const int quarter = warp & 3, half = warp >> 2;
         uint8_t *os = out_stage + warp * kOutBytes;   // [row][32 columns]
-        if (!q.p.offsets) grid_dep_wait();
         while (true) {
             const OutTile t = next_tile();
             // zeros: an expert without rows, or a part of a short sum

@@ -768,6 +768,26 @@ def test_a_wait_that_runs_out_is_reported(call, counts, n, k):
     assert nv.products_status() == 0
 
 
+@pytest.mark.parametrize("rows,n,k", [(6000, 1536, 512), (300, 256, 4104), (257, 200, 264)], ids=["many tiles", "a split sum", "few tiles"])
+@pytest.mark.parametrize("call", ["fwd", "dx", "dw"])
+def test_a_wait_that_runs_out_leaves_the_next_call_alone(call, rows, n, k):
+    """A dense call enqueued right behind a stalled one starts before that has ended, on the SMs that it leaves free; its
+    own bounded waits must not run meanwhile."""
+    x, dy, w = normal((rows, k), BF16, 231), normal((rows, n), BF16, 232), normal((n, k), BF16, 233, 0.1)
+    run = {"fwd": lambda: nv.grouped_gemm(x, w), "dx": lambda: nv.grouped_gemm_dx(dy, w), "dw": lambda: nv.grouped_gemm_dw(dy, x)}[call]
+    few, one = normal((500, 264), BF16, 234), normal((2, 200, 264), BF16, 235)
+    off = offsets_of((200, 300))
+    want = run()
+    nv.grouped_gemm(few, one, off)
+    assert nv.products_status() == 0
+    nv.nvfp4_moe_test_products_stall(1)
+    nv.grouped_gemm(few, one, off)
+    got = run()
+    assert nv.products_status() == -8
+    assert torch.equal(got, want)
+    assert nv.products_status() == 0
+
+
 def test_calls_from_several_threads():
     import threading
     run, _ = _all_calls(rows=200, n=264, k=328, seed=181)
