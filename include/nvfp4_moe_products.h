@@ -105,7 +105,8 @@ NVFP4_MOE_API int nvfp4_moe_quantize_int8(const nvfp4_moe_quantize_io *io, void 
  *   type         of x, dy and w: BF16, F16, or (grouped_gemm only) INT8
  *   x_scale      INT8: [rows] f32;  w_scale  INT8: [groups][n] f32; else not read.
  *                out[p][j] = x_scale[p] * w_scale[e][j] * sum_k x[p][k] w[e][j][k],
- *                the sum exact in 32-bit integers
+ *                the sum exact in 32-bit integers; the scales may be of any size (no
+ *                product of theirs leaves FP32's range unless the result does)
  *   out_type     BF16, F16 or F32; 16-bit sums are FP32, rounded once to out_type
  *   accumulate   nonzero: out += result, F32 outputs only
  * x, dy and w must be 16-byte aligned and their row strides a multiple of 16 bytes;

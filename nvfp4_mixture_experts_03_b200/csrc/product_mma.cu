@@ -156,6 +156,11 @@ __device__ inline void left_stage(int lane) {
     __syncwarp();
 }
 
+// One column: this thread gets its lane's.
+__device__ inline void tmem_ld1(uint32_t taddr, uint32_t &r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+
 // 16 lanes x 32 columns as fragments: registers 4i..4i+3 hold, of columns 8i + 2 (lane % 4)
 // and the one after it, lane row lane / 4 and then row lane / 4 + 8.
 __device__ inline void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[16]) {
@@ -673,7 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Scales of int8 products come in while the sums are still being formed: of the
             // columns and rows that a fragment gives this lane, or of its column and row.
             float cs[4], rs[kBatches][kF32 ? 1 : 16];
-            if (kI8 && t.e >= 0) {
+            float check[1 + kAccCols / 64];   // every scale of the warp's columns and rows, a lane each
+            if (kI8 && !kSplit && t.e >= 0) {
                 const float *ws = q.p.w_scale + (int64_t)t.e * q.p.n, *xs = q.p.x_scale + t.row0;
 #pragma unroll
                 for (int j = 0; j < 4; j++) cs[j] = ws[min(kF32 ? col : col0 + 8 * j + (lane >> 2), cols - 1)];
@@ -682,6 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < (kF32 ? 1 : 16); j++)
                         rs[h][j] = xs[min(kBatch * (2 * h + half) + (kF32 ? lane : 8 * (j >> 1) + 2 * (lane & 3) + (j & 1)), t.nrow - 1)];
+                check[0] = ws[min(col, cols - 1)];
+#pragma unroll
+                for (int j = 0; j < kAccCols / 64; j++)
+                    check[1 + j] = xs[min(kBatch * (2 * (j * 32 / kBatch) + half) + j * 32 % kBatch + lane, t.nrow - 1)];
             }
             const int buf = it & 1;
             if (t.e < 0 || (!none && !warp_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, 5))) break;
@@ -703,8 +713,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) arrive_leader<CG>(&bars->acc_empty[buf], rank);
             };
-            if (kBatch * half >= t.nrow) release();
             const uint32_t tbase = tmem_base + buf * kAccCols + ((uint32_t)(quarter * 32) << 16);
+            // int8: are any scales of the warp's part of the tile not of usual size? Then the tile, a rare
+            // one, is written here, a row at a time. Asked once a tile, and only when its first sums have
+            // been read and the scales have had time to come in (pair by pair in the loops below, 64
+            // experts, 20011 rows took 61 us instead of 49).
+            auto unusual_scales = [&]() {
+                bool usual = true;
+#pragma unroll
+                for (int j = 0; j < 1 + kAccCols / 64; j++) usual &= usual_scale(check[j]);
+                if (__all_sync(0xffffffffu, usual)) return false;
+                const float c = q.p.w_scale[(int64_t)t.e * q.p.n + min(col, cols - 1)];
+#pragma unroll 1
+                for (int r = kBatch * half; r < t.nrow; r += (r + 1) % kBatch ? 1 : kBatch + 1) {
+                    uint32_t u;
+                    __syncwarp();
+                    tmem_ld1(tbase + r, u);
+                    tmem_ld_wait();
+                    if (col >= cols) continue;
+                    const float v = scaled((int32_t)u, q.p.x_scale[t.row0 + r], c);
+                    const int64_t at = (orow + r) * q.p.out_ld + col;
+                    if constexpr (kF32) {
+                        float *o = static_cast<float *>(q.p.out) + at;
+                        *o = q.p.out_add ? *o + v : v;
+                    } else
+                        static_cast<uint16_t *>(q.p.out)[at] =
+                            (uint16_t)(q.out_type == NVFP4_MOE_TYPE_BF16 ? pack_bf16(v, 0.0f) : pack_f16(v, 0.0f));
+                }
+                release();
+                return true;
+            };
+            if (kBatch * half >= t.nrow) release();
 #pragma unroll
             for (int h = 0; h < kBatches; h++) {
                 const int r = kBatch * (2 * h + half);
@@ -723,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int b = 0; b < 2; b++) tmem_ld_frag(tbase + ((uint32_t)(16 * b) << 16) + r + 32 * s, f[s][b]);
                         tmem_ld_wait();
                     }
+                    if (kI8 && h == 0 && unusual_scales()) break;
                     if (last) release();
                     uint32_t w[8][4];   // [8 rows][8 columns], two rows to a word
 #pragma unroll
@@ -732,8 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t *u = &f[i >> 2][j >> 1][4 * (i & 3) + 2 * (j & 1)];
                             float v0 = __uint_as_float(u[0]), v1 = __uint_as_float(u[1]);
                             if (kI8) {
-                                v0 = (float)(int32_t)u[0] * (rs[h][2 * i] * cs[j]);
-                                v1 = (float)(int32_t)u[1] * (rs[h][2 * i + 1] * cs[j]);
+                                v0 = scaled_usual((int32_t)u[0], rs[h][2 * i], cs[j]);
+                                v1 = scaled_usual((int32_t)u[1], rs[h][2 * i + 1], cs[j]);
                             }
                             w[i][j] = none ? 0u : q.out_type == NVFP4_MOE_TYPE_BF16 ? pack_bf16(v0, v1) : pack_f16(v0, v1);
                         }
@@ -771,11 +811,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(tbase + r, u);
                         tmem_ld_wait();
                     }
+                    if (kI8 && h == 0 && unusual_scales()) break;
                     if (last) release();
 #pragma unroll
                     for (int j = 0; j < 32; j++)
                         v[j] = none ? 0.0f
-                               : kI8 ? (float)(int32_t)u[j] * (__shfl_sync(0xffffffffu, rs[h][0], j) * cs[0])
+                               : kI8 ? scaled_usual((int32_t)u[j], __shfl_sync(0xffffffffu, rs[h][0], j), cs[0])
                                      : __uint_as_float(u[j]);
                     if (q.staged && n == kBatch) {
                         left_stage(lane);
@@ -851,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int o = 1; o < 8; o++)
                         if (o < q.split) u = kI8 ? u + w[j][o] : __float_as_uint(__uint_as_float(u) + __uint_as_float(w[j][o]));
                     float v = __uint_as_float(u);
-                    if (kI8) v = (float)(int32_t)u * (q.p.x_scale[mine.row0 + row] * cs);
+                    if (kI8) v = scaled((int32_t)u, q.p.x_scale[mine.row0 + row], cs);
                     const int64_t at = ((MODE == kDw ? (int64_t)mine.e * q.p.n : 0) + mine.row0 + row) * q.p.out_ld + col;
                     if constexpr (kF32) {
                         float *out = static_cast<float *>(q.p.out) + at;

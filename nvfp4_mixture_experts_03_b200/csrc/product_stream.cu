@@ -157,8 +157,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) produ
         Acc sum = part[0][r][c];
 #pragma unroll
         for (int w = 1; w < kWarps; w++) sum += part[w][r][c];
-        float v = (float)sum;
-        if (kI8) v *= p.x_scale[row0 + r] * p.w_scale[(int64_t)e * p.n + col];
+        float v;
+        if constexpr (kI8)
+            v = scaled(sum, p.x_scale[row0 + r], p.w_scale[(int64_t)e * p.n + col]);
+        else
+            v = sum;
         const int64_t at = (row0 + r) * p.out_ld + col;
         if (out_type == NVFP4_MOE_TYPE_F32)
             put(static_cast<float *>(p.out) + at, v, p.out_add);

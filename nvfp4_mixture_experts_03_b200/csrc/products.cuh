@@ -41,6 +41,19 @@ __device__ inline __half from_f32(float v) { return __float2half_rn(v); }
 template <>
 __device__ inline float from_f32(float v) { return v; }
 
+// An exact int8 sum times its two scales. Their own product may leave FP32's range where the
+// result does not (1e-30 * 1e-10 is subnormal, 1e25 * 1e25 infinite, and 0 * inf NaN), so unless
+// both are of usual size the smaller one goes first: |sum| is 0 or at least 1, so sum * smaller
+// loses nothing to underflow that the scale had not lost, and overflows only where the result
+// does. Scales of usual size keep the one multiplication less on the way from the sum.
+__device__ inline bool usual_scale(float v) { return v == 0.0f || (fabsf(v) >= 0x1p-40f && fabsf(v) <= 0x1p40f); }
+__device__ inline float scaled_usual(int32_t sum, float a, float b) { return (float)sum * (a * b); }
+__device__ inline float scaled(int32_t sum, float a, float b) {
+    if (usual_scale(a) && usual_scale(b)) return scaled_usual(sum, a, b);
+    const bool first = fabsf(a) < fabsf(b);
+    return (float)sum * (first ? a : b) * (first ? b : a);
+}
+
 // The products follow one another in short chains, and a small one's launch and start take
 // as long as its work: each is a programmatic dependent of the kernel before it in the
 // stream, lets its own dependents launch at once, and waits for that kernel, all of it,

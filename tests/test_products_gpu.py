@@ -159,6 +159,65 @@ def test_int8_dense(rows, n, k):
     assert_within(out, total, 4 * 2.0 ** -24 * ref.abs() + 2.0 ** -24 * (total.abs() + 2.0 ** -20 * ref.abs()), "int8 accumulated")
 
 
+@pytest.mark.parametrize("rows,n,k", [(1, 48, 128), (20, 136, 256), (300, 264, 512), (600, 256, 8208)], ids=["token", "streamed", "tiles", "a split sum"])
+@pytest.mark.parametrize("xs,ws", [(1e-30, 1e-10), (3e-38, 2e-5), (1e-41, 1e3), (1e33, 1e-33), (1e-33, 1e33), (1e25, 1e25), (-1e30, 1e-30),
+                                   (1.2e-38, -1.2e-38), (3e38, 1e-44)])
+def test_int8_scales_of_any_size(rows, n, k, xs, ws):
+    """float(sum) and its two products round once each: 3 * 2^-24 of the value, 4 of them with room for the second order;
+    a result below 2^-126 may lose half a step of 2^-149 (the first product is a whole multiple of that step, so it is
+    exact wherever it is subnormal). A sum of zero gives zero, whatever the scales. The values pass FP32's largest number
+    where the definition does."""
+    x, w = codes((rows, k), 241), codes((n, k), 242)
+    x[rows // 2] = 0
+    w[n // 3] = 0
+    vary = torch.linspace(0.75, 1.0, rows, device=DEV, dtype=torch.float64)
+    xs = (vary * xs).float()
+    ws = torch.full((n,), ws, device=DEV)
+    ref = (x.double() @ w.double().T) * xs[:, None].double() * ws.double()
+    most = torch.finfo(F32).max
+    near = ((ref.abs() / most - 1).abs() < 1e-5)
+    for out_dtype in (F32, BF16):
+        got = nv.gemm_int8(x, w, xs, ws, out_dtype=out_dtype).double()
+        assert (got[rows // 2] == 0).all() and (got[:, n // 3] == 0).all()
+        inside = ref.abs() < torch.finfo(out_dtype).max * (1 - 2.0 ** -6)
+        outside = (ref.abs() > most) & ~near
+        assert (got[outside] == ref[outside].sign() * math.inf).all()
+        tol = 4 * 2.0 ** -24 * ref.abs() + 2.0 ** -150 + (half_step(out_dtype, ref) * (1 + 2.0 ** -8) if out_dtype != F32 else 0)
+        assert_within(got[inside], ref[inside], tol[inside], f"scales to {out_dtype}")
+
+
+@pytest.mark.parametrize("counts,n,k", [((2, 1, 0, 3), 77, 200), ((300, 0, 33, 400), 200, 264), ((1300, 700), 520, 1040)],
+                         ids=["streamed", "tiles", "pairs"])
+def test_int8_rows_with_unusual_scales_beside_others(counts, n, k):
+    """A few rows far too small or too large, a NaN and zeros among usual ones: the usual rows keep their bits, the others are
+    within four roundings (below 2^-126: within half a step of 2^-149), also where they are added to something."""
+    off, rows, E = offsets_of(counts), sum(counts), len(counts)
+    x, w = codes((rows, k), 243), codes((E, n, k), 244)
+    xs, ws = torch.rand(rows, generator=gen(245), device=DEV) + 0.5, torch.rand(E, n, generator=gen(246), device=DEV) + 0.5
+    ws[:, n // 2] = 1e-12
+    usual = {o: nv.grouped_gemm(x, w, off, x_scale=xs, w_scale=ws, out_dtype=o) for o in (F32, BF16)}
+    odd = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    odd[::5] = True
+    odd[-1] = True
+    some = xs.clone()
+    some[::5] = torch.tensor([1e-36, 1e30, 2e-41], device=DEV).repeat(rows)[: some[::5].numel()]
+    some[-1] = NAN
+    y, _ = ref_fwd(x, w, off.tolist())
+    for e, (lo, hi) in enumerate(zip(off.tolist()[:-1], off.tolist()[1:])):
+        y[lo:hi] *= some[lo:hi, None].double() * ws[e].double()
+    for o in (F32, BF16):
+        got = nv.grouped_gemm(x, w, off, x_scale=some, w_scale=ws, out_dtype=o)
+        assert torch.equal(got[~odd], usual[o][~odd])
+        assert got[-1].isnan().all()
+        tol = 4 * 2.0 ** -24 * y[:-1].abs() + 2.0 ** -150 + (half_step(o, y[:-1]) * (1 + 2.0 ** -8) if o != F32 else 0)
+        assert_within(got[:-1], y[:-1], tol, f"to {o}")
+    base = torch.randn(rows, n, generator=gen(247), device=DEV)
+    out = base.clone()
+    nv.grouped_gemm(x, w, off, x_scale=some, w_scale=ws, out=out, accumulate=True)
+    total = y[:-1] + base[:-1].double()
+    assert_within(out[:-1], total, 4 * 2.0 ** -24 * y[:-1].abs() + 2.0 ** -24 * (total.abs() + 2.0 ** -20 * y[:-1].abs()), "added")
+
+
 @pytest.mark.parametrize("rows", [1, 24, 200])
 def test_int8_sums_are_exact_up_to_the_last_k(rows):
     """All codes -128 at the largest k: every sum is 2^14 * 131071, just below 2^31; with one code of x
