@@ -70,20 +70,40 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) produ
     int e = 0, row0 = blockIdx.y * 8 * NT, end = p.rows;
     if (p.offsets) {
         row0 = blockIdx.y;
-        int below = 0;
-        for (int i = threadIdx.x; i < p.groups; i += kThreads) below += p.offsets[i] <= row0;
+        // Offsets clamped into the rows and to no less than those before them: the group is the one
+        // ahead of the first offset past row0, and starts at the largest of those up to it. In order,
+        // those are all that are not past row0.
+        int first = p.groups + 1, below = 0, lo = 0;
+        for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
+            const int v = p.offsets[i];
+            if (v > row0)
+                first = min(first, i);
+            else {
+                below++;
+                lo = max(lo, v);
+            }
+        }
+        __shared__ int3 found[kWarps];
+        first = __reduce_min_sync(0xffffffffu, first);
         below = __reduce_add_sync(0xffffffffu, below);
-        __shared__ int count[kWarps];
-        if ((threadIdx.x & 31) == 0) count[threadIdx.x >> 5] = below;
+        lo = __reduce_max_sync(0xffffffffu, lo);
+        if ((threadIdx.x & 31) == 0) found[threadIdx.x >> 5] = make_int3(first, below, lo);
         __syncthreads();
         below = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) below += count[w];
-        if (below == 0) return;
-        e = below - 1;
-        const int lo = max(p.offsets[e], 0);
-        end = min(p.offsets[e + 1], p.rows);
-        if (row0 < lo || row0 >= end || (row0 - lo) % (8 * NT)) return;
+        for (int w = 0; w < kWarps; w++) {
+            first = min(first, found[w].x);
+            below += found[w].y;
+            lo = max(lo, found[w].z);
+        }
+        if (first == 0 || first > p.groups) return;
+        if (below != first) {   // out of order
+            lo = 0;
+            for (int i = 0; i < first; i++) lo = max(lo, p.offsets[i]);
+        }
+        e = first - 1;
+        end = min(p.offsets[first], p.rows);
+        if ((row0 - lo) % (8 * NT)) return;
     }
     const int nrow = min(8 * NT, end - row0);
 

@@ -487,6 +487,32 @@ def test_wrong_offsets_stay_in_range():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("off", [[0, 50, 200, 300], [-7, 20, 10, 100], [90, 40, 1 << 30, 3], [2 ** 31 - 1, -2 ** 31, 50, 100],
+                                 [30, 10, 20, 60], [0, 60, 59, 61], [5, 99, 98, 97], [-1, -2, -3, -4], [100, 100, 100, 100], [0, 0, 7, 5]])
+@pytest.mark.parametrize("n,k", [(64, 64), (1024, 64), (64, 1024)])
+def test_wrong_offsets_are_clamped_alike_in_every_kernel(off, n, k):
+    """The same rows for the same offsets, whichever kernel takes the call: each offset clamped into [0, rows] and to no less
+    than those before it. (100 rows of 64 columns are streamed, of 1024 not.)"""
+    rows, E = 100, 3
+    x, dy, w = normal((rows, k), BF16, 251), normal((rows, n), BF16, 252), normal((E, n, k), BF16, 253, 0.1)
+    clamped, top = [], 0
+    for v in off:
+        top = max(top, min(max(v, 0), rows))
+        clamped.append(top)
+    off = torch.tensor(off, dtype=torch.int32, device=DEV)
+    for fn, a, m, cols in ((nv.grouped_gemm, x, w, n), (nv.grouped_gemm_dx, dy, w.transpose(1, 2), k)):
+        out = torch.full((rows, cols), 7.0, device=DEV)
+        fn(a, w, off, out=out)
+        y, s = ref_fwd(a, m, clamped)
+        mine = ~y.isnan().any(1)
+        assert (out[~mine] == 7.0).all()
+        assert_within(out[mine], y[mine], tol16(a.shape[1], s[mine], y[mine], F32), fn.__name__)
+    dw = nv.grouped_gemm_dw(dy, x, off)
+    for e, (lo, hi) in enumerate(zip(clamped[:-1], clamped[1:])):
+        a, b = dy[lo:hi].double(), x[lo:hi].double()
+        assert_within(dw[e], a.T @ b, tol16(max(hi - lo, 1), a.abs().T @ b.abs(), a.T @ b, F32), f"dw of {e}")
+
+
 def test_element_offsets_past_32_bits():
     """Rows whose elements start past 2^31 from the first, in x and in the output, and matrices that do."""
     k, ld = 136, (1 << 26) + 8
