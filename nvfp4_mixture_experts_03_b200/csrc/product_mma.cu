@@ -43,6 +43,10 @@ constexpr int kTilesAhead = 4;          // tiles that the tile warp lists ahead
 constexpr int kMaxStages = 10;
 constexpr int kBand = 8;                // row tiles of a band (Tiles::at)
 constexpr size_t kSmemLimit = 227 * 1024;
+// Bounds of the waits: for what takes a stage's time, and on top of it for what takes a tile's
+// whole sum, which may be long (2^30 rows of one group: 2^24 stages, over 3 s of one CTA; a stage
+// takes some 0.2 to 0.4 us).
+constexpr uint64_t kWaitNs = 2000000000ull, kStageNs = 4000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr uint64_t kSettleNs = 1000000ull;   // lets in-flight copies land after an abort
 
@@ -59,6 +63,7 @@ struct MmaParams {
     int32_t split;         // one-CTA tiles: CTAs of a cluster that share a tile's sum (1: none)
     int32_t staged;        // whole batches of outputs leave as boxes (map_o is set); rows are 16-byte aligned
     int32_t stall;         // test hook: the first CTA makes no copies
+    uint64_t sum_ns;       // bound of a wait for a tile's sum
     int32_t a_whole, b_whole;   // M- or N-major operands: all of a stage's 64-column boxes as one
 };
 
@@ -278,9 +283,9 @@ __device__ inline int uni(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 // A bounded wait by a whole warp, with one answer for all its lanes.
 template <bool kCluster>
-__device__ inline bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where) {
+__device__ inline bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int where, uint64_t limit_ns = kWaitNs) {
     if (__all_sync(0xffffffffu, mbar_try_wait<kCluster>(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, abort, g_status, where));
+    return __all_sync(0xffffffffu, mbar_wait<kCluster>(bar, parity, abort, g_status, where, limit_ns));
 }
 
 template <int MODE, int CG>
@@ -465,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto next_tile = [&]() {
         OutTile t;
         t.e = -1;
-        if (warp_wait<false>(&bars->tile_full[slot], slot_phase, abort, 7)) {
+        if (warp_wait<false>(&bars->tile_full[slot], slot_phase, abort, 7, q.sum_ns)) {
             t = groups.ahead[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->tile_empty[slot]);
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (t.c && (left & 15)) {
                     const int last = (stage + steps - 1) % S;
                     const uint32_t parity = (tail_phase >> last) & 1;
-                    if (!warp_wait<false>(&bars->tail[last], parity, abort, 4)) break;
+                    if (!warp_wait<false>(&bars->tail[last], parity, abort, 4, q.sum_ns)) break;
                     tail_phase ^= 1u << last;
                     uint8_t *a = smem + last * stage_size, *b = a + kABytes;
                     const int pad = 16 - (left & 15), nb = cdiv(half, 64);   // rows to zero, in each 64-column box
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // (the first kTilesAhead slots are free: no wait on the clock)
             if (!q.p.offsets && round == kTilesAhead) grid_dep_wait();
-            if (!warp_wait<false>(&bars->tile_empty[slot], slot_phase ^ 1, abort, 8)) break;
+            if (!warp_wait<false>(&bars->tile_empty[slot], slot_phase ^ 1, abort, 8, q.sum_ns)) break;
             if (lane == 0) {
                 groups.ahead[slot] = t;
                 mbar_arrive(&bars->tile_full[slot]);
@@ -694,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     check[1 + j] = xs[min(kBatch * (2 * (j * 32 / kBatch) + half) + j * 32 % kBatch + lane, t.nrow - 1)];
             }
             const int buf = it & 1;
-            if (t.e < 0 || (!none && !warp_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, 5))) break;
+            if (t.e < 0 || (!none && !warp_wait<CG == 2>(&bars->acc_full[buf], (acc_phase >> buf) & 1, abort, 5, q.sum_ns))) break;
             if (none && q.p.out_add && !kSplit) continue;
             if (!none) {
                 it++;
@@ -1136,6 +1141,7 @@ cudaError_t launch_product_mma(int mode, const Product &p, nvfp4_moe_type type, 
     if (ok && q.staged) ok = map_output(&o, p.out, out, out_rows, cols, p.out_ld);
     if (!ok) return cudaErrorInvalidValue;
     q.split = shape.split;
+    q.sum_ns = kWaitNs + kStageNs * cdiv(cdiv(mode == kFwd ? p.k : mode == kDx ? p.n : p.rows, i8 ? 128 : 64), q.split);
     if (g_stall > 0) {
         g_stall--;
         q.stall = 1;

@@ -545,6 +545,22 @@ def test_element_offsets_past_32_bits():
     assert not dw[:-1].any()
 
 
+def test_dw_of_the_most_rows_in_one_of_many_groups():
+    """2^30 rows, all but a few of them in one of 1024 groups: a single CTA's sum of more than three seconds."""
+    rows, c, E, e = nv.products.MAX_EXTENT, 8, nv.products.MAX_GROUPS, 700
+    x, dy = (torch.zeros(rows, c, dtype=BF16, device=DEV) for _ in range(2))
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[: e + 1], off[e + 1:] = 5, rows - 3
+    some = torch.tensor([5, 6, 63, 64, 2 ** 21 + 3, 2 ** 29, rows - 70, rows - 5, rows - 4], device=DEV)
+    x[some] = torch.randint(-4, 5, (some.numel(), c), generator=gen(261), device=DEV).to(BF16)
+    dy[some] = torch.randint(-4, 5, (some.numel(), c), generator=gen(262), device=DEV).to(BF16)
+    x[:5], dy[:5], x[-3:], dy[-3:] = NAN, NAN, NAN, NAN
+    dw = nv.grouped_gemm_dw(dy, x, off)
+    assert nv.products_status() == 0
+    assert torch.equal(dw[e], dy[some].float().T @ x[some].float())
+    assert not dw[:e].any() and not dw[e + 1:].any()
+
+
 def test_values_outside_a_groups_rows_do_not_reach_it():
     """NaN and infinities in the neighbouring expert's rows and matrices stay there."""
     counts, n, k = (70, 33, 100), 200, 136
