@@ -66,7 +66,9 @@ typedef enum {
  *   rows, cols   rows >= 0 (0 is a no-op), cols >= 1 codes per row
  *   in_type      BF16, F16 or F32
  *   swiglu       0: the row's values are v = in[row][0..cols)
- *                1: in rows hold gate | up, 2*cols values; v = SiLU(gate) * up in FP32
+ *                1: in rows hold gate | up, 2*cols values; v = SiLU(gate) * up in FP32,
+ *                to 2^-20 of the value for gates from -87 on (below, SiLU is under
+ *                2^-119 and is taken for 0)
  *   in_stride    elements from one row to the next, >= the row's values
  *   q, q_stride  [rows][cols] int8, q_stride >= cols; bytes past cols are not written;
  *                q must not overlap in

@@ -50,6 +50,22 @@ __device__ inline float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// SiLU(g) * u = g / (1 + e^-g) * u, right to some ten units of 2^-24. e^x as 2^y with y = x log2(e)
+// rounded, times e^(x - y ln 2), whose exponent is taken in two parts of ln 2 (Cody and Waite's
+// reduction) and is so small that 1 + it will do: without it the rounding of y alone costs |x| units
+// (the layer's silu() leaves it out: a row of strongly negative gates only was coded from values
+// 2^-18 off; 8191 x 768 BF16 6.9 us with it, 7.2 with this one, 8.3 with expf). Past +-88 the sum is
+// 1, or so large that its inverse is 0; g itself still carries NaN and infinities on.
+__device__ inline float swiglu(float g, float u) {
+    constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f, kLn2Rest = (float)(0.693147180559945309 - (double)kLn2);
+    const float x = -fminf(fmaxf(g, -88.0f), 88.0f), y = x * kLog2e;
+    float e, inv;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
+    e = fmaf(e, fmaf(-y, kLn2Rest, fmaf(-y, kLn2, x)), e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(1.0f + e));
+    return g * inv * u;
+}
+
 // Eight values of a row as a thread keeps them: 16-bit ones as read, else FP32.
 template <typename T, bool kSwiglu>
 struct Chunk {
@@ -127,7 +143,7 @@ __device__ inline void load_chunk(Chunk<T, kSwiglu> &k, const T *in, int c, int 
         load8<T, kVec>(in, c, cols, g);
         load8<T, kVec>(in + cols, c, cols, u);
 #pragma unroll
-        for (int i = 0; i < 8; i++) k.w[i] = __float_as_uint(silu(__uint_as_float(g[i])) * __uint_as_float(u[i]));
+        for (int i = 0; i < 8; i++) k.w[i] = __float_as_uint(swiglu(__uint_as_float(g[i]), __uint_as_float(u[i])));
     }
 }
 template <typename T, bool kSwiglu>
@@ -138,7 +154,7 @@ __device__ inline void form_chunk(Chunk<T, kSwiglu> &k) {
         for (int i = 0; i < 8; i++) r[i] = k.w[i];
         const T *g = reinterpret_cast<const T *>(r), *u = reinterpret_cast<const T *>(r + 4);
 #pragma unroll
-        for (int i = 0; i < 8; i++) k.w[i] = __float_as_uint(silu(to_f32(g[i])) * to_f32(u[i]));
+        for (int i = 0; i < 8; i++) k.w[i] = __float_as_uint(swiglu(to_f32(g[i]), to_f32(u[i])));
     }
 }
 

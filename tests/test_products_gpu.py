@@ -404,6 +404,42 @@ def test_swiglu_quantize(dtype, rows, cols):
     assert (q[torch.arange(rows, device=DEV), h.abs().argmax(1)].abs() == 127).all()
 
 
+@pytest.mark.parametrize("lo,hi", [(-87.0, -60.0), (-60.0, -30.0), (-30.0, -10.0), (-87.0, -86.0), (-5.0, 5.0), (20.0, 88.0)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_swiglu_values_at_every_gate(dtype, lo, hi):
+    """Rows of one value, whose scale is |SiLU(g) u| / 127, and rows of many such values, which their codes show. In units of
+    2^-24: the exponential is off by up to 4 (2^-22.5 and a rounding), 1 + it by 1, its inverse by 2, the products with g and u by 1
+    each, the scale's quotient by 1: 10, below 2^-20."""
+    rows = 4000
+    g = (torch.rand(rows, generator=gen(271), device=DEV, dtype=torch.float64) * (hi - lo) + lo).to(dtype)
+    u = ((torch.rand(rows, generator=gen(272), device=DEV, dtype=torch.float64) + 0.5) * 1e3).to(dtype)
+    h = g.double() * torch.sigmoid(g.double()) * u.double()
+    q, scale = nv.quantize_int8(torch.stack([g, u], 1).contiguous(), swiglu=True)
+    assert ((scale.double() * 127 - h.abs()).abs() <= 2.0 ** -20 * h.abs()).all()
+    assert torch.equal(q[:, 0], (h.sign() * 127).to(torch.int8))
+    wide = torch.cat([g.view(40, 100), u.view(40, 100)], 1)
+    q, scale = nv.quantize_int8(wide, swiglu=True)
+    t = h.view(40, 100) / (h.view(40, 100).abs().amax(1, keepdim=True) / 127)
+    assert ((q.double() - t).abs() <= 0.5 + 127 * 2.0 ** -19).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_swiglu_rows_at_the_ends_of_the_range(dtype):
+    """Gates of any size, infinities and NaN, each with ordinary, huge and non-finite ups: a row that holds something not finite,
+    or whose value passes FP32's largest number, has scale NaN and code 0; else its scale is that of the definition, or 0 below -87."""
+    inf = math.inf
+    pairs = [(g, u) for g in (-inf, inf, NAN, -3e38, 3e38, -1e30, 1e30, -88.5, -87.5, -87.0, 88.0, 89.0, 0.0, -0.0)
+             for u in (1.0, 0.0, -2.0, inf, -inf, NAN, 1e30)]
+    x = torch.tensor(pairs, device=DEV).to(dtype)
+    q, scale = nv.quantize_int8(x, swiglu=True)
+    g, u = x.double().unbind(1)
+    h = (g * torch.sigmoid(g) * u).abs()
+    bad = ~x.isfinite().all(1) | ~(h <= torch.finfo(F32).max)
+    assert scale[bad].isnan().all() and (q[bad] == 0).all()
+    near = (scale.double() * 127 - h).abs() <= 2.0 ** -20 * h
+    assert (near | ((g < -87) & (scale == 0)))[~bad].all()
+
+
 def test_swiglu_quantize_far_gates():
     """Gates whose exponential leaves FP32 either way: SiLU is 0 or the gate itself."""
     g = torch.tensor([[-1e30, -200.0, -89.0, -87.5, 200.0, 1e5, 0.0, 88.9]], device=DEV)
