@@ -16,11 +16,13 @@ are allocated on it.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
+import os
 import struct
 
 import torch
 
-from . import OK, NVFP4MoEError, lib
+from . import OK, NVFP4MoEError, build, lib
 
 TYPE_BF16, TYPE_F16, TYPE_F32, TYPE_INT8 = 0, 1, 2, 3
 INT8_MAX_K = 131071
@@ -89,10 +91,21 @@ _pack_gemm = struct.Struct("@7iPPqPPqPqPPq").pack     # GemmIO
 _pack_quantize = struct.Struct("@4iPqPqP").pack       # QuantizeIO
 
 
-try:      # csrc/marshal.cpp: the common calls, natively; without it they take the Python below
-    from . import _marshal
-except ImportError:
-    _marshal = None
+def _load_marshal():
+    """csrc/marshal.cpp: the common calls, natively; without it they take the Python below."""
+    path = build.marshal_path()
+    if not os.path.exists(path):
+        return None
+    spec = importlib.util.spec_from_file_location(f"{__package__}._marshal", path)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError:
+        return None
+    return module
+
+
+_marshal = _load_marshal()
 _native = None   # _marshal, once the library is loaded
 
 

@@ -166,3 +166,37 @@ def _t(*shape, dtype=torch.bfloat16):
 def test_python_calls_refuse(call):
     with pytest.raises((ValueError, nv.NVFP4MoEError)):
         call()
+
+
+def test_the_library_is_built_without_the_binding(monkeypatch, tmp_path, capsys):
+    """No compiler, no headers, no torch: the library is built all the same, and first."""
+    from nvfp4_mixture_experts_03_b200 import build
+    monkeypatch.setattr(build, "marshal_path", lambda: str(tmp_path / "none.so"))
+    monkeypatch.setenv("CXX", "/bin/false")
+    seen = []
+    monkeypatch.setattr(build, "build_library", lambda *a: seen.append(a) or build.LIB)
+    assert build.build() == build.LIB and len(seen) == 1
+    assert "binding" in capsys.readouterr().err
+
+
+def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
+    from nvfp4_mixture_experts_03_b200 import build
+    import sysconfig
+    assert products._load_marshal() is not None
+    assert build.marshal_path().endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert products._load_marshal() is None
+
+
+def test_the_binding_follows_every_header(monkeypatch):
+    """Newer than its source and one header, older than the other that it includes: built again."""
+    import os
+    from nvfp4_mixture_experts_03_b200 import build
+    path = build.build_marshal()
+    called = []
+    monkeypatch.setattr(build.subprocess, "check_call", lambda cmd: called.append(cmd) or open(cmd[cmd.index("-o") + 1], "wb").close())
+    monkeypatch.setattr(build.os, "replace", lambda a, b: os.unlink(a))
+    assert build.build_marshal() == path and not called
+    real = os.path.getmtime
+    monkeypatch.setattr(build.os.path, "getmtime", lambda p: real(p) + (1e6 if p.endswith("nvfp4_moe.h") else 0))
+    assert build.build_marshal() == path and len(called) == 1
