@@ -12,6 +12,8 @@
 // barrier but the one before the join. Many warps with a few loads each in flight do better
 // than few with many (1 x 8192 x 8192 BF16: 19.7 us, 6.8 TB/s, with 2 pieces a lane and 4 CTAs an
 // SM; 26.0 with 4 pieces and 3 CTAs), as long as the loop that needs no masks has none.
+#include <algorithm>
+
 #include "products.cuh"
 
 namespace nvmoe {
@@ -210,12 +212,19 @@ cudaError_t launch(const Product &p, nvfp4_moe_type out, cudaStream_t s) {
 // 16 columns of each; the tensor-core tiles have some 6 us of start and end. Measured against
 // them (us, streamed / tiles, BF16): dense 8 x 8192 x 8192 20 / 30, 32 x the same 35 / 31, 64 x 1536 x
 // 2048 6.5 / 10.6, 64 x 2560 x 2560 10.7 / 12.0, 128 x 2048 x 768 7.4 / 7.5, 201 x the same 11.1 / 7.6, 32 x
-// 8192 x 256 5.0 / 6.1, 64 x the same 8.4 / 6.1; by group 32 rows of 8 x 1536 x 2048 10.5 / 10.7, 64 of
-// them 15.4 / 10.7, 32 of 64 x 1536 x 2048 27 / 34, 64 of 16 x 512 x 512 5.5 / 7.2, 128 of them 8.1 / 7.2.
+// 8192 x 256 5.0 / 6.1, 64 x the same 8.4 / 6.1.
+// By group a CTA stands for every row and 16 columns, so their number counts, the more the
+// longer the offsets that each looks through; where a row is long, the tiles wait for the matrices
+// too. Measured over 12 sizes of matrices in BF16 and int8, 2 to 512 groups, 1 to 192 rows (us,
+// streamed / tiles; rows to the left of the bar are streamed): BF16 8 x 1536 x 2048 24: 11.2 / 12.0 | 48:
+// 15.2 / 12.6; 512 x 2048 x 768 8: 7.8 / 7.1 | 24: 19.4 / 12.1; 512 x 1536 x 2048 16: 20.2 / 20.0 | 32:
+// 32.0 / 33.7; 2 x 256 x 256 128: 4.7 / 4.8 | 192: 6.2 / 4.9; int8 64 x 1536 x 2048 24: 15.1 / 14.3 | 32:
+// 17.8 / 15.9; 8 x 2048 x 768 16: 6.5 / 6.5 | 24: 7.9 / 6.8. On average over all of them the rule costs
+// 0.8 % more than the better kernel, at worst 31 % (3100 CTAs whatever the row and the groups: 2 and 65 %).
 bool product_streams(int mode, const Product &p, int elem_bytes) {
     if (mode != kFwd) return false;
     const int64_t blocks = cdiv(p.n, kCols);
-    if (p.offsets) return p.rows * blocks <= 3100;
+    if (p.offsets) return p.rows * blocks <= (p.groups <= 128 ? 2000 : 1200) + std::min<int64_t>((int64_t)p.k * elem_bytes, 8192) / 4;
     if (p.rows <= 8) return true;
     const int64_t passes = cdiv(p.rows, 32);
     return passes * blocks <= 512 && passes * p.n * p.k * elem_bytes <= 30000000;
