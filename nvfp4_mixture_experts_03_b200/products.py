@@ -11,7 +11,12 @@ the next product's input.
 Every call enqueues on `stream` (default: torch's current stream on the tensors' device),
 never synchronises, and raises NVFP4MoEError for what the library refuses. Given another
 stream than the current one, keep the inputs alive until it is done with them; outputs
-are allocated on it.
+are allocated on it. What goes wrong on the device, a product's bounded wait that gave up,
+is told by `products_status()`.
+
+Nothing is recorded for autograd: outputs are detached, whatever the inputs require. The
+gradients are calls of their own, for a torch.autograd.Function or a training step that is
+written out.
 """
 from __future__ import annotations
 
@@ -22,7 +27,7 @@ import struct
 
 import torch
 
-from . import OK, NVFP4MoEError, build, lib
+from . import ERR, OK, NVFP4MoEError, build, lib
 
 TYPE_BF16, TYPE_F16, TYPE_F32, TYPE_INT8 = 0, 1, 2, 3
 INT8_MAX_K = 131071
@@ -209,6 +214,9 @@ def _new(shape, dtype, index: int, stream):
 
 
 def _failed(rc: int, what: str):
+    if ERR.get(rc) == "MISALIGNED":
+        what += " (operands of a product start every row on a multiple of 16 bytes: copy into a matrix with padded rows," \
+                " torch.empty(rows, padded)[:, :cols]; outputs, scales and offsets on one of their type's size)"
     raise NVFP4MoEError(rc, what)
 
 
@@ -357,6 +365,8 @@ def grouped_gemm_dw(dy, x, offsets=None, *, out=None, out_dtype=None, accumulate
     if dy_rows != rows:
         _refuse(f"dy, x: {dy_rows} and {rows} rows")
     groups = 1 if offsets is None else offsets.numel() - 1
+    if groups < 1:
+        _refuse("offsets: expected one more than there are groups")
     off = _offsets(offsets, groups, index)
     if out is None and out_dtype is None:
         out_dtype = torch.float32

@@ -952,6 +952,49 @@ def test_calls_from_several_threads():
             assert torch.equal(a, b)
 
 
+def test_calls_from_several_threads_on_their_current_streams():
+    """The native calls, which drop the interpreter lock: each thread with a current stream of its own."""
+    import threading
+    run, _ = _all_calls(rows=200, n=264, k=328, seed=191)
+    want = run()
+    torch.cuda.synchronize()
+    assert nv.products._native is not None
+    got, errors = [[] for _ in range(4)], []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i].append(run())
+            s.synchronize()
+        except Exception as e:      # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for g in got:
+        assert len(g) == 20
+        for outs in g:
+            for a, b in zip(outs, want):
+                assert torch.equal(a, b)
+
+
+def test_outputs_are_detached_and_empty_offsets_refused():
+    x, w = normal((30, 64), BF16, 281), torch.nn.Parameter(normal((2, 40, 64), BF16, 282))
+    off = offsets_of((10, 20))
+    y = nv.grouped_gemm(x, w, off)
+    assert not y.requires_grad
+    assert torch.equal(y, nv.grouped_gemm(x, w.detach(), off))
+    for n in (0, 1):
+        with pytest.raises(ValueError, match="offsets"):
+            nv.grouped_gemm_dw(y, x, torch.zeros(n, dtype=torch.int32, device=DEV))
+
+
 # --------------------------------------------------- together, as they are used
 
 def test_shared_expert_in_8_bits_beside_the_routed_layer():

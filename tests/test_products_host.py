@@ -168,6 +168,15 @@ def test_python_calls_refuse(call):
         call()
 
 
+def test_what_is_misaligned_is_said():
+    with pytest.raises(nv.NVFP4MoEError, match="16 bytes.*MISALIGNED") as e:
+        products._failed(MISALIGNED, "nvfp4_moe_grouped_gemm")
+    assert e.value.code == MISALIGNED
+    with pytest.raises(nv.NVFP4MoEError) as e:
+        products._failed(DIMS, "nvfp4_moe_grouped_gemm")
+    assert "16 bytes" not in str(e.value)
+
+
 def test_the_library_is_built_without_the_binding(monkeypatch, tmp_path, capsys):
     """No compiler, no headers, no torch: the library is built all the same, and first."""
     from nvfp4_mixture_experts_03_b200 import build
