@@ -72,39 +72,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2) produ
     int e = 0, row0 = blockIdx.y * 8 * NT, end = p.rows;
     if (p.offsets) {
         row0 = blockIdx.y;
-        // Offsets clamped into the rows and to no less than those before them: the group is the one
-        // ahead of the first offset past row0, and starts at the largest of those up to it. In order,
-        // those are all that are not past row0.
-        int first = p.groups + 1, below = 0, lo = 0;
-        for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
+        // The group is the one ahead of the first offset past row0: as many are not, if they are in
+        // order (the count's upper half: how many are not in order).
+        int found = 0;
+        for (int i = threadIdx.x; i < p.groups; i += kThreads) {
             const int v = p.offsets[i];
-            if (v > row0)
-                first = min(first, i);
-            else {
-                below++;
-                lo = max(lo, v);
-            }
+            found += (v <= row0) + (v > p.offsets[i + 1] ? 1 << 16 : 0);
         }
-        __shared__ int3 found[kWarps];
-        first = __reduce_min_sync(0xffffffffu, first);
-        below = __reduce_add_sync(0xffffffffu, below);
-        lo = __reduce_max_sync(0xffffffffu, lo);
-        if ((threadIdx.x & 31) == 0) found[threadIdx.x >> 5] = make_int3(first, below, lo);
+        found = __reduce_add_sync(0xffffffffu, found);
+        __shared__ int count[kWarps];
+        if ((threadIdx.x & 31) == 0) count[threadIdx.x >> 5] = found;
         __syncthreads();
-        below = 0;
+        found = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            first = min(first, found[w].x);
-            below += found[w].y;
-            lo = max(lo, found[w].z);
+        for (int w = 0; w < kWarps; w++) found += count[w];
+        int lo = 0;
+        if (found >> 16) {   // out of order: each clamped to no less than those before it
+            found = 0;
+            while (found < p.groups && p.offsets[found] <= row0) lo = max(lo, p.offsets[found++]);
         }
-        if (first == 0 || first > p.groups) return;
-        if (below != first) {   // out of order
-            lo = 0;
-            for (int i = 0; i < first; i++) lo = max(lo, p.offsets[i]);
-        }
-        e = first - 1;
-        end = min(p.offsets[first], p.rows);
+        if (found == 0) return;
+        e = found - 1;
+        lo = max(lo, p.offsets[e]);
+        end = min(p.offsets[found], p.rows);
+        if (row0 >= end) return;
         if ((row0 - lo) % (8 * NT)) return;
     }
     const int nrow = min(8 * NT, end - row0);
