@@ -207,15 +207,16 @@ cudaError_t launch(const Product &p, nvfp4_moe_type out, cudaStream_t s) {
 // By group a CTA stands for every row and 16 columns, so their number counts, the more the
 // longer the offsets that each looks through; where a row is long, the tiles wait for the matrices
 // too. Measured over 12 sizes of matrices in BF16 and int8, 2 to 512 groups, 1 to 192 rows (us,
-// streamed / tiles; rows to the left of the bar are streamed): BF16 8 x 1536 x 2048 24: 11.2 / 12.0 | 48:
-// 15.2 / 12.6; 512 x 2048 x 768 8: 7.8 / 7.1 | 24: 19.4 / 12.1; 512 x 1536 x 2048 16: 20.2 / 20.0 | 32:
-// 32.0 / 33.7; 2 x 256 x 256 128: 4.7 / 4.8 | 192: 6.2 / 4.9; int8 64 x 1536 x 2048 24: 15.1 / 14.3 | 32:
-// 17.8 / 15.9; 8 x 2048 x 768 16: 6.5 / 6.5 | 24: 7.9 / 6.8. On average over all of them the rule costs
-// 0.8 % more than the better kernel, at worst 31 % (3100 CTAs whatever the row and the groups: 2 and 65 %).
+// streamed / tiles; rows to the left of the bar are streamed): BF16 8 x 1536 x 2048 32: 12.1 / 12.7 | 48:
+// 14.1 / 12.7; 512 x 2048 x 768 8: 7.0 / 7.1 | 16: 13.0 / 9.9; 512 x 1536 x 2048 24: 24.3 / 25.5 | 32:
+// 29.8 / 34.0; 2 x 256 x 256 128: 4.2 / 4.7 | 192: 5.5 / 4.9; int8 64 x 1536 x 2048 24: 14.6 / 14.3 | 32:
+// 17.2 / 15.9; 8 x 2048 x 768 16: 6.0 / 6.5 | 24: 7.2 / 6.9. On average over all of them the rule costs 0.8 %
+// more than the better kernel, at worst 39 % (all rows in one of 512 groups); 3100 CTAs whatever
+// the row and the groups cost 1.2 and 47 %.
 bool product_streams(int mode, const Product &p, int elem_bytes) {
     if (mode != kFwd) return false;
     const int64_t blocks = cdiv(p.n, kCols);
-    if (p.offsets) return p.rows * blocks <= (p.groups <= 128 ? 2000 : 1200) + std::min<int64_t>((int64_t)p.k * elem_bytes, 8192) / 4;
+    if (p.offsets) return p.rows * blocks <= (p.groups <= 128 ? 2200 : 1200) + std::min<int64_t>((int64_t)p.k * elem_bytes, 4096) / 3;
     if (p.rows <= 8) return true;
     const int64_t passes = cdiv(p.rows, 32);
     return passes * blocks <= 512 && passes * p.n * p.k * elem_bytes <= 30000000;
