@@ -268,7 +268,7 @@ cudaError_t launch(const nvfp4_moe_quantize_io &io, cudaStream_t s) {
     // A warp a row where there are rows enough to fill the GPU that way, else a CTA (us, warps /
     // CTAs a row: 1000 x 768 BF16 2.3 / 2.2, 2048 x 768 2.6 / 3.3, 8192 x 768 6.3 / 10.5; 4096 x 2048
     // 8.7 / 8.4, 32768 x 2048 35 / 50, FP32 55 / 60). h of more than 1024 columns takes too many
-    // registers of a warp (32768 x 2048 SwiGLU of BF16 125 / 67).
+    // registers of a warp (32768 x 2048 SwiGLU of BF16 125 / 67, now 74).
     const int chunks = cdiv(io.cols, 8);
     if (chunks <= 32 && io.rows >= 8)
         return launch_as<T, kSwiglu, kVec, 32, 1>(io, s);
